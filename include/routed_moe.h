@@ -354,6 +354,112 @@ MOE_API int32_t moe_combine_rows(const void* y, int32_t R, const int32_t* row_of
 MOE_API int32_t moe_rmsnorm(const void* x, const float* gamma, float eps, int32_t T, int32_t H,
                     void* xn, void* stream);
 
+/* ---------------------------------------------------------------- narrow formats (MX)
+ * Microscaled operands for the experts: 32 consecutive elements of a row (a
+ * block) share one power of two 2^p, p in [-127, 127], held as the byte
+ * p + 127 (UE8M0).  Elements are E4M3 (MOE_MXFP8, largest 448) or E2M1
+ * (MOE_MXFP4, largest 6).  The pages ship bf16 experts; these forms are the
+ * library's own, for callers that trade accuracy for weight and activation
+ * bytes, and the tensor cores read both operands as they are.
+ *   codes   uint8 [rows, K] (MOE_MXFP8), or [rows, K/2] with two elements per
+ *           byte, the even one in the low nibble (MOE_MXFP4)
+ *   scales  uint8 [ceil(K/128)][rows][4]: the byte of block b of row r at
+ *           [b/4][r][b%4]; bytes of blocks past K must be 0
+ * A stack of matrices [G, rows, K] has G such arrays of each, one after the
+ * other.  K is a multiple of 32 (<= 16384).  codes, bf16 inputs and xn are
+ * 16-byte aligned, bf16 outputs of products 32-byte, scales 4-byte
+ * (MOE_ERR_INVALID_ARG).  Forward only, like the block itself. */
+typedef enum {
+  MOE_MXFP8 = 1, /* E4M3 elements */
+  MOE_MXFP4 = 2  /* E2M1 elements */
+} moe_mx_format_t;
+
+/* x -> MX.  A block's p is the smallest integer with max|v| <= largest * 2^p,
+ * at least -127 (no element saturates); elements are rounded once, to nearest,
+ * ties to the even code.  A block that holds a NaN or an infinity gets the
+ * scale byte 255 (NaN) and codes 0: every product with it is NaN.
+ *   x      device bf16 [groups, rows, K]
+ *   codes, scales  out, as above (bytes of blocks past K are written as 0) */
+MOE_API int32_t moe_mx_quantize(const void* x, int32_t groups, int32_t rows, int32_t K,
+                                int32_t fmt, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* MX -> bf16: x = bf16(element * 2^p), NaN for a block of scale byte 255.
+ * Exact for what moe_mx_quantize gives, except below bf16's smallest value. */
+MOE_API int32_t moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t groups,
+                                  int32_t rows, int32_t K, int32_t fmt, void* x, void* stream);
+
+/* RMSNorm with the residual's addition before it and, if wanted, an MX output
+ * after it (one pass; fp32 accumulation as moe_rmsnorm):
+ *   sum = bf16( x + residual ),  xn = bf16( sum * (mean(sum^2) + eps)^(-1/2) * gamma ),
+ *   (codes, scales) = MX(xn), bit for bit moe_mx_quantize of xn
+ *   x        device bf16 [T,H]; residual device bf16 [T,H] or NULL (0)
+ *   gamma    device fp32 [H] (16-byte aligned) or NULL (1); eps >= 0
+ *   sum      device bf16 [T,H] out or NULL; may be x or residual (in place)
+ *   xn       device bf16 [T,H] out, or NULL when codes are wanted alone
+ *   fmt      0: no codes (codes, scales NULL); MOE_MXFP8 or MOE_MXFP4
+ * H a multiple of 64 (<= 16384).  A row's outputs depend on that row alone. */
+MOE_API int32_t moe_add_rmsnorm(const void* x, const void* residual, const float* gamma,
+                                float eps, int32_t T, int32_t H, int32_t fmt, void* sum, void* xn,
+                                uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Workspace bytes of moe_grouped_mm / moe_grouped_mm_mx; 0 for invalid sizes. */
+MOE_API size_t moe_grouped_mm_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K);
+MOE_API size_t moe_grouped_mm_mx_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K);
+
+/* Product of rows grouped by expert with their expert's matrix, ragged groups:
+ *   y[r] = bf16( x[r] . W_e^T )  for r in [offsets[e], offsets[e+1]), fp32 accumulation
+ *   x       device bf16 [R,K]; w device bf16 [E,N,K]; y device bf16 [R,N]
+ *   offsets device int32 [E+1], non-decreasing, 0 <= offsets[0], offsets[E] <= R
+ *           (empty groups allowed; rows outside the groups are left as they were)
+ * E in 1..128; N and K multiples of 32 (<= 16384).  Offsets that break their
+ * rule leave MOE_ERR_DEVICE_INDEX in the status word (moe_read_device_status)
+ * and y undefined; no access leaves the operands.  y must not overlap x or w. */
+MOE_API int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R, int32_t E,
+                               int32_t N, int32_t K, const void* w, void* y, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* The same with both operands in one MX format (block-scaled tensor-core
+ * products, fp32 accumulation, one rounding to bf16):
+ *   y[dest(r)] = bf16( row_w[r] * sum_b 2^(p_x[r,b] + p_w[e,n,b]) sum_{k in b} x[r,k] w[e,n,k] )
+ *   x_codes, x_scales  device, R rows of K elements
+ *   w_codes, w_scales  device, a stack of E matrices of N rows of K elements
+ *   row_w    device fp32 [R] or NULL (1)
+ *   row_dest device int32 [R], distinct rows of y, or NULL (dest(r) = r); a row
+ *            whose destination lies outside [0, y_rows) is not stored
+ *   y        device bf16 [y_rows, N] (y_rows >= R without row_dest)
+ * Offsets, sizes, errors and workspace as moe_grouped_mm. */
+MOE_API int32_t moe_grouped_mm_mx(const uint8_t* x_codes, const uint8_t* x_scales,
+                                  const int32_t* offsets, int32_t R, int32_t E, int32_t N,
+                                  int32_t K, int32_t fmt, const uint8_t* w_codes,
+                                  const uint8_t* w_scales, const float* row_w,
+                                  const int32_t* row_dest, void* y, int32_t y_rows,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of moe_expert_rows_mx (gathered: 1 when tok_of is given); 0
+ * for invalid sizes. */
+MOE_API size_t moe_expert_rows_mx_workspace_bytes(int32_t R, int32_t H, int32_t E, int32_t I,
+                                                  int32_t fmt, int32_t gathered);
+
+/* moe_expert_rows with narrow rows and weights: for expert e and each row r in
+ * [offsets[e], offsets[e+1])
+ *   h = MX( silu(x_r.Wg_e^T) * (x_r.Wu_e^T) ),  y[dest(r)] = bf16( row_w[r] * h . W2_e^T )
+ * with h quantised from the fp32 product in the format of the operands.
+ *   x_codes, x_scales  device, T rows of H elements
+ *   tok_of   device int32 [R]: x_r is row tok_of[r] of x (a token outside [0, T)
+ *            counts as zeros); NULL: x holds the rows already grouped, T == R
+ *   w13_*    E matrices [2I, H], gate rows then up rows; w2_* E matrices [H, I]
+ *   row_w, row_dest, y, y_rows, offsets and errors as moe_grouped_mm_mx
+ * H and I multiples of 32 (<= 16384).  With row_dest = t*top_k + j and
+ * moe_combine_rows this is the routed half of the block on narrow operands. */
+MOE_API int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int32_t T,
+                                   const int32_t* tok_of, const int32_t* offsets, int32_t R,
+                                   int32_t E, int32_t H, int32_t I, int32_t fmt,
+                                   const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                   const uint8_t* w2_codes, const uint8_t* w2_scales,
+                                   const float* row_w, const int32_t* row_dest, void* y,
+                                   int32_t y_rows, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 /* Waits for stream, then reads and clears the device status word that the
  * kernels of moe_forward / moe_permute leave in workspace (MOE_OK, or the
  * first device-side error of the last call).  *site receives where the

@@ -652,6 +652,61 @@ int32_t forward_fp8_impl(const void* x, const float* Wr, const float* bias, cons
   return MOE_OK;
 }
 
+// ------------------------------------------------------------------ MX operands
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+bool mx_fmt_ok(int32_t fmt) { return fmt == MOE_MXFP8 || fmt == MOE_MXFP4; }
+
+// A matrix of rows x K elements, or a stack of them.
+int32_t check_mx(int32_t groups, int32_t rows, int32_t K, int32_t fmt) {
+  if (groups < 0 || rows < 0 || K <= 0 || !mx_fmt_ok(fmt)) return MOE_ERR_INVALID_ARG;
+  if (K % 32 != 0 || K > MAX_DIM) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+// y [R,N] = rows [R,K] times the matrix [N,K] of their group.
+int32_t check_grouped(int32_t R, int32_t E, int32_t N, int32_t K) {
+  if (R < 0 || E <= 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (E > MAX_E || N % 32 != 0 || K % 32 != 0 || N > MAX_DIM || K > MAX_DIM ||
+      R > INT32_MAX / 2)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+// What the two products of MX operands have in common; the caller fills in the end.
+MxGemmArgs mx_args(const uint8_t* a_scales, const int32_t* offsets, int32_t R, int32_t E,
+                   int32_t K, int32_t fmt, const uint8_t* b_scales, int* status) {
+  MxGemmArgs g;
+  memset(&g, 0, sizeof(g));
+  g.offsets = offsets;
+  g.groups = E;
+  g.rows = R;
+  g.a_scales = reinterpret_cast<const uint32_t*>(a_scales);
+  g.b_scales = reinterpret_cast<const uint32_t*>(b_scales);
+  g.words = mx_words(K);
+  g.k_bytes = mx_row_bytes(K, fmt);
+  g.status = status;
+  g.timeout_ns = DEFAULT_TIMEOUT_NS;
+  return g;
+}
+
+struct MxExpertsLayout {
+  size_t x, xs, h, hs, total;
+};
+
+// Status, the gathered rows and their scales, h and its scales.
+MxExpertsLayout mx_experts_layout(int32_t R, int32_t H, int32_t I, int32_t fmt, bool gathered) {
+  MxExpertsLayout L;
+  const size_t r = R;
+  size_t off = align_up(sizeof(DevStatus));
+  L.x = off;  off += align_up(gathered ? r * mx_row_bytes(H, fmt) : 0);
+  L.xs = off; off += align_up(gathered ? r * mx_words(H) * 4 : 0);
+  L.h = off;  off += align_up(r * mx_row_bytes(I, fmt));
+  L.hs = off; off += align_up(r * mx_words(I) * 4);
+  L.total = off;
+  return L;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1032,6 +1087,195 @@ int32_t moe_rmsnorm(const void* x, const float* gamma, float eps, int32_t T, int
   if (T == 0) return MOE_OK;
   if (!x || !xn) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_rmsnorm(x, gamma, eps, T, H, xn, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t moe_add_rmsnorm(const void* x, const void* residual, const float* gamma, float eps,
+                        int32_t T, int32_t H, int32_t fmt, void* sum, void* xn, uint8_t* codes,
+                        uint8_t* scales, void* stream) {
+  if (T < 0 || H <= 0 || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (H % 64 != 0 || H > MAX_DIM) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (fmt != 0 && !mx_fmt_ok(fmt)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || (!xn && !codes)) return MOE_ERR_INVALID_ARG;
+  if ((fmt != 0) != (codes != nullptr) || (fmt != 0) != (scales != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(sum, 16) ||
+      !aligned(xn, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  // every row is read before it is written, so sum may be x or the residual;
+  // no other output may be anything else that the call reads or writes
+  if (xn && (xn == x || xn == residual || xn == sum)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_add_rmsnorm(x, residual, gamma, eps, T, H, fmt, sum, xn, codes, scales,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+int32_t moe_mx_quantize(const void* x, int32_t groups, int32_t rows, int32_t K, int32_t fmt,
+                        uint8_t* codes, uint8_t* scales, void* stream) {
+  const int32_t st = check_mx(groups, rows, K, fmt);
+  if (st != MOE_OK) return st;
+  if (groups == 0 || rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || codes == x) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_mx_quantize(x, groups, rows, K, fmt, codes, scales,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+int32_t moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t groups,
+                          int32_t rows, int32_t K, int32_t fmt, void* x, void* stream) {
+  const int32_t st = check_mx(groups, rows, K, fmt);
+  if (st != MOE_OK) return st;
+  if (groups == 0 || rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || codes == x) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_mx_dequantize(codes, scales, groups, rows, K, fmt, x,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_grouped_mm_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K) {
+  if (check_grouped(R, E, N, K) != MOE_OK) return 0;
+  // status, the checked offsets and the tile prefix [E+1]
+  return align_up(sizeof(DevStatus)) + 2 * align_up((size_t)(E + 1) * 4);
+}
+
+int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R, int32_t E, int32_t N,
+                       int32_t K, const void* w, void* y, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  const int32_t st = check_grouped(R, E, N, K);
+  if (st != MOE_OK) return st;
+  if (R == 0) return MOE_OK;
+  if (!x || !offsets || !w || !y || y == x || y == w) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 32)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(workspace, workspace_bytes, moe_grouped_mm_workspace_bytes(R, E, N, K)))
+    return MOE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* status = at<int>(workspace, 0);
+  int* start = at<int>(workspace, align_up(sizeof(DevStatus)));
+  int* tiles = at<int>(workspace, align_up(sizeof(DevStatus)) + align_up((size_t)(E + 1) * 4));
+  RMOE_TRY(launch_group_schedule(offsets, E, R, start, tiles, status, s));
+  GemmArgs g;
+  memset(&g, 0, sizeof(g));
+  g.status = status;
+  g.timeout_ns = DEFAULT_TIMEOUT_NS;
+  g.alt_group = -1;
+  g.row_start = start;
+  g.num_groups = E;
+  g.k_steps = (K + 63) / 64;  // past K both operands' tiles read zeros
+  g.out = static_cast<__nv_bfloat16*>(y);
+  g.ldo = N;
+  g.n_valid = N;
+  g.dest_mul = 1;  // output row = row
+  const int sms = num_sms();
+  CUtensorMap tm_w, tm_x;
+  RMOE_TRY(make_tmap_3d(&tm_w, w, E, N, K));
+  if ((int64_t)R <= 64LL * E) {  // few rows per expert: swapped operands, as moe_expert_rows
+    const int chunk = (int64_t)R <= 20LL * E ? 32 : 128;
+    RMOE_TRY(make_tmap_2d_box(&tm_x, x, R, K, 32));
+    g.n_tiles = (N + 127) / 128;
+    g.n_out_tile = 128;
+    const long long items = (R / chunk + E + 1LL) * g.n_tiles;
+    return cuda_status(launch_grouped_gemm_swap(EPI_ROWSCALE, chunk, tm_w, tm_x, tm_w, tm_x, g,
+                                                (int)std::min<long long>(sms, items), s));
+  }
+  RMOE_TRY(make_tmap_2d(&tm_x, x, R, K));
+  g.mtile_start = tiles;
+  g.n_tiles = (N + 255) / 256;
+  g.n_out_tile = 256;
+  g.b_second = 128;
+  const long long ctas = 2LL * (R / MTILE + E) * g.n_tiles;
+  return cuda_status(launch_grouped_gemm(EPI_ROWSCALE, tm_x, tm_w, tm_x, tm_w, g,
+                                         (int)std::min<long long>(sms, ctas), s));
+}
+
+size_t moe_grouped_mm_mx_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K) {
+  if (check_grouped(R, E, N, K) != MOE_OK) return 0;
+  return align_up(sizeof(DevStatus));
+}
+
+int32_t moe_grouped_mm_mx(const uint8_t* x_codes, const uint8_t* x_scales, const int32_t* offsets,
+                          int32_t R, int32_t E, int32_t N, int32_t K, int32_t fmt,
+                          const uint8_t* w_codes, const uint8_t* w_scales, const float* row_w,
+                          const int32_t* row_dest, void* y, int32_t y_rows, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const int32_t st = check_grouped(R, E, N, K);
+  if (st != MOE_OK) return st;
+  if (!mx_fmt_ok(fmt) || y_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (R == 0) return MOE_OK;
+  if (!x_codes || !x_scales || !offsets || !w_codes || !w_scales || !y || y == x_codes ||
+      y == w_codes)
+    return MOE_ERR_INVALID_ARG;
+  if (!row_dest && y_rows < R) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(y, 32) || !aligned(x_scales, 4) ||
+      !aligned(w_scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(workspace, workspace_bytes, moe_grouped_mm_mx_workspace_bytes(R, E, N, K)))
+    return MOE_ERR_WORKSPACE;
+  MxGemmArgs g = mx_args(x_scales, offsets, R, E, K, fmt, w_scales, at<int>(workspace, 0));
+  g.n_rows = N;
+  g.n_valid = N;
+  g.row_w = row_w;
+  g.row_dest = row_dest;
+  g.out_rows = y_rows;
+  g.out = y;
+  g.clear_status = 1;
+  return cuda_status(launch_grouped_mx(fmt, MX_ROWS, x_codes, w_codes, g,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_expert_rows_mx_workspace_bytes(int32_t R, int32_t H, int32_t E, int32_t I, int32_t fmt,
+                                          int32_t gathered) {
+  if (check_grouped(R, E, I, H) != MOE_OK || !mx_fmt_ok(fmt)) return 0;
+  return mx_experts_layout(R, H, I, fmt, gathered != 0).total;
+}
+
+int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int32_t T,
+                           const int32_t* tok_of, const int32_t* offsets, int32_t R, int32_t E,
+                           int32_t H, int32_t I, int32_t fmt, const uint8_t* w13_codes,
+                           const uint8_t* w13_scales, const uint8_t* w2_codes,
+                           const uint8_t* w2_scales, const float* row_w, const int32_t* row_dest,
+                           void* y, int32_t y_rows, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  const int32_t st = check_grouped(R, E, I, H);
+  if (st != MOE_OK) return st;
+  if (!mx_fmt_ok(fmt) || T < 0 || y_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (R == 0) return MOE_OK;
+  if (!x_codes || !x_scales || !offsets || !w13_codes || !w13_scales || !w2_codes || !w2_scales ||
+      !y || y == x_codes)
+    return MOE_ERR_INVALID_ARG;
+  if ((!tok_of && T != R) || (!row_dest && y_rows < R)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x_codes, 16) || !aligned(w13_codes, 16) || !aligned(w2_codes, 16) ||
+      !aligned(y, 32) || !aligned(x_scales, 4) || !aligned(w13_scales, 4) ||
+      !aligned(w2_scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  const MxExpertsLayout L = mx_experts_layout(R, H, I, fmt, tok_of != nullptr);
+  if (!ws_ok(workspace, workspace_bytes, L.total)) return MOE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* status = at<int>(workspace, 0);
+  const uint8_t *a = x_codes, *as = x_scales;
+  if (tok_of) {  // the tokens' narrow rows in expert order
+    uint8_t* g = at<uint8_t>(workspace, L.x);
+    uint8_t* gs = at<uint8_t>(workspace, L.xs);
+    RMOE_TRY(launch_gather_mx(x_codes, x_scales, tok_of, T, R, mx_row_bytes(H, fmt), mx_words(H),
+                              g, gs, s));
+    a = g;
+    as = gs;
+  }
+  uint8_t* h = at<uint8_t>(workspace, L.h);
+  uint8_t* hs = at<uint8_t>(workspace, L.hs);
+  MxGemmArgs up = mx_args(as, offsets, R, E, H, fmt, w13_scales, status);
+  up.n_rows = 2 * I;
+  up.n_valid = I;
+  up.out = h;
+  up.out_scales = reinterpret_cast<uint32_t*>(hs);
+  up.clear_status = 1;
+  RMOE_TRY(launch_grouped_mx(fmt, MX_SWIGLU, a, w13_codes, up, s));
+  MxGemmArgs dn = mx_args(hs, offsets, R, E, I, fmt, w2_scales, status);
+  dn.n_rows = H;
+  dn.n_valid = H;
+  dn.row_w = row_w;
+  dn.row_dest = row_dest;
+  dn.out_rows = y_rows;
+  dn.out = y;
+  return cuda_status(launch_grouped_mx(fmt, MX_ROWS, h, w2_codes, dn, s));
 }
 
 int32_t moe_read_device_status(void* workspace, int32_t* site, void* stream) {

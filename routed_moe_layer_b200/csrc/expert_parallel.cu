@@ -64,6 +64,74 @@ __global__ void __launch_bounds__(32)
   }
 }
 
+// tile_prefix on checked offsets: one warp, each lane's groups in order; the
+// running maximum of the offsets makes them non-decreasing.
+__global__ void __launch_bounds__(32)
+    group_schedule_kernel(const int* __restrict__ offsets, int groups, int rows,
+                          int* __restrict__ start, int* __restrict__ tiles,
+                          int* __restrict__ status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int PER = 5;  // offsets per lane (up to 160)
+  const int lane = threadIdx.x;
+  if (lane == 0) {
+    status[0] = 0;
+    status[1] = 0;
+  }
+  int raw[PER], top = 0;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int g = lane * PER + q;
+    raw[q] = g <= groups ? offsets[g] : 0;
+    top = max(top, min(max(raw[q], 0), rows));
+  }
+  int before = top;  // largest offset of the lanes before this one
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, off);
+    if (lane >= off) before = max(before, v);
+  }
+  before = __shfl_up_sync(0xffffffffu, before, 1);
+  if (lane == 0) before = 0;
+  int at[PER], sum = 0;
+  bool bad = false;
+  int run = before;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int g = lane * PER + q;
+    if (g <= groups) {
+      run = max(run, min(max(raw[q], 0), rows));
+      bad |= run != raw[q];
+      start[g] = run;
+    }
+    at[q] = run;
+  }
+  // tiles of group g - 1 lie between offsets g - 1 and g
+  int prev = __shfl_up_sync(0xffffffffu, at[PER - 1], 1);
+  int loc[PER];
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int g = lane * PER + q;
+    loc[q] = g > 0 && g <= groups ? (at[q] - prev + MTILE - 1) / MTILE : 0;
+    sum += loc[q];
+    prev = at[q];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  int total = incl - sum;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int g = lane * PER + q;
+    total += loc[q];
+    if (g <= groups) tiles[g] = total;
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) report_error(status, MOE_ERR_DEVICE_INDEX, 70);
+}
+
 // One warp per token (small batches: up to H/256 warps, each on every
 // parts-th 512-byte column block); 16-byte loads and stores.
 __global__ void __launch_bounds__(256)
@@ -124,6 +192,13 @@ cudaError_t launch_rows_expert_ids(const int* offsets, int E, int R, int* ids,
 cudaError_t launch_tile_prefix(const int* offsets, int groups, int* tiles, cudaStream_t stream) {
   if (groups < 1 || groups > 159) return cudaErrorInvalidValue;
   return launch_chained(tile_prefix_kernel, dim3(1), dim3(32), 0, stream, offsets, groups, tiles);
+}
+
+cudaError_t launch_group_schedule(const int* offsets, int groups, int rows, int* start,
+                                  int* tiles, int* status, cudaStream_t stream) {
+  if (groups < 1 || groups > 159) return cudaErrorInvalidValue;
+  return launch_chained(group_schedule_kernel, dim3(1), dim3(32), 0, stream, offsets, groups, rows,
+                        start, tiles, status);
 }
 
 cudaError_t launch_combine_rows(const void* y, int R, const int* row_of, int top_k, int T, int H,

@@ -1,0 +1,641 @@
+// Grouped products of MX operands (mx_format.cuh) on the sm_100a tensor cores:
+// for every row r of group e
+//   D[r, n] = sum_b 2^(pa[r,b] + pw[e,n,b]) * sum_{k in block b} a[r,k] * w[e,n,k]
+// with the block-scaled tcgen05.mma, which reads 8- or 4-bit elements from
+// shared memory and their scales from TMEM and accumulates in fp32, and three
+// ends:
+//   MX_ROWS    out[dest(r), n] = bf16( row_w[r] * D[r, n] )   (dest(r) = r, row_w = 1
+//              where they are not given)
+//   MX_SWIGLU  h[r, i] = silu(D[r, i]) * D[r, I + i], quantised in the format of the
+//              operands: 32 columns of a row are one block, which one epilogue
+//              thread holds in registers, so h never exists in a wider type.
+//
+// Shape: persistent clusters of two CTAs share one pair MMA (cta_group::2) of
+// 256 rows x 256 columns; a K step is 128 bytes of every row: 128 elements
+// (MXFP8, 4 MMAs of K = 32) or 256 (MXFP4, 4 MMAs of K = 64).  Bytes a step and
+// MMA time a step are those of the bf16 kernel (grouped_gemm.cu), for two and
+// four times the elements.  Each CTA loads its 128 rows of A and half of the B
+// tile; the scales of both (its own rows' for A, all 256 columns' for B) come
+// by 4-byte cp.async straight into the layout that tcgen05.cp moves to TMEM:
+// 16-byte row l holds the words of tile rows l, l+32, l+64, l+96.
+// Warp roles (both CTAs):
+//   warp 0      TMA loads of A and B (counted on the leader CTA's barrier)
+//   warp 1      TMEM; in the leader one thread copies the scales to TMEM and
+//               issues the MMAs
+//   warps 2..9  epilogue, as in grouped_gemm.cu
+//   warps 10,11 scales of A and of B
+// TMEM: columns 0..255 the accumulator, 256 + 32 s.. the scales of stage s.
+// The accumulator is not double-buffered (two of them leave no columns for the
+// scales); the epilogue reads it whole into registers and hands it back before
+// it computes or stores anything.
+// Every wait is bounded (common.cuh).
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "mx_format.cuh"
+
+namespace rmoe {
+
+namespace {
+
+constexpr int BM = 128;          // rows per CTA
+constexpr int TILE_M = 2 * BM;   // rows per pair tile
+constexpr int BN = 256;          // accumulator columns
+constexpr int KB = 128;          // bytes of a row per K step
+constexpr int STAGES = 6;
+constexpr int A_BYTES = BM * KB;
+constexpr int B_BYTES = BN / 2 * KB;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int SF_BYTES = 512;    // scale words of 128 rows
+constexpr int THREADS = 384;
+constexpr int EPI_WARPS = 8;
+constexpr int SF_LAG = 2;        // K steps of scales in flight per warp
+constexpr int MAX_GROUPS = 128;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TMEM_SF = 256;        // first scale column
+constexpr uint32_t TMEM_SF_STAGE = 32;   // columns per stage: A's words at +0, B's at +8
+constexpr uint32_t TMEM_SFB = 8;
+constexpr unsigned FULL = 0xffffffffu;
+
+template <int FMT>
+struct Fmt {
+  static constexpr int kWords = FMT == MOE_MXFP8 ? 1 : 2;  // scale words per row and K step
+  static constexpr int kSf = kWords * 3 * SF_BYTES;        // A, then both halves of B
+  static constexpr size_t kSmem = 1024 + (size_t)STAGES * (STAGE_BYTES + kSf);
+};
+
+struct __align__(8) SmemTail {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t tfull;
+  uint64_t tempty;
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int bad_offsets;
+  int mt_start[MAX_GROUPS + 1];
+  int row_start[MAX_GROUPS + 1];
+};
+
+__device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity,
+                                                uint64_t timeout_ns) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (globaltimer_ns() - t0 > timeout_ns) return;
+  }
+}
+
+struct Tile {
+  int g, row0, rows, nt;
+};
+
+__device__ __forceinline__ Tile tile_at(int tile, int n_tiles, int groups, const int* mts,
+                                        const int* rs) {
+  Tile t;
+  const int mt = tile / n_tiles;
+  t.nt = tile - mt * n_tiles;
+  int lo = 0, hi = groups;  // largest g with mts[g] <= mt (skips empty groups)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (mts[mid] <= mt)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  t.g = lo;
+  t.row0 = rs[lo] + (mt - mts[lo]) * TILE_M;
+  t.rows = min(TILE_M, rs[lo + 1] - t.row0);
+  return t;
+}
+
+// The same expression as in the bf16 kernels.
+__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// Block-scaled pair MMA.  Element and scale formats in idesc: A and B E4M3
+// with one scale per 32 of K = 32 (MXFP8), or E2M1 with two of K = 64 (MXFP4).
+template <int FMT>
+__device__ __forceinline__ void umma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (FMT == MOE_MXFP8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor without the scale ids: UE8M0 scales, M = 256, N = 256.
+template <int FMT>
+__device__ constexpr uint32_t idesc_mx() {
+  return (FMT == MOE_MXFP4 ? (1u << 7) | (1u << 10) : 0u)  // E2M1 (0: E4M3)
+         | (static_cast<uint32_t>(BN >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(TILE_M >> 4) << 24);
+}
+
+// MMA kk of a K step uses scale byte kk (MXFP8) or bytes 2*(kk%2).. (MXFP4).
+__device__ __forceinline__ uint32_t idesc_sf(uint32_t idesc, uint32_t id) {
+  return idesc | (id << 4) | (id << 29);
+}
+
+// 32 rows of 16 bytes to 4 TMEM columns, repeated in the four lane quarters, in
+// both CTAs of the pair from the same shared-memory offset.
+__device__ __forceinline__ void tmem_copy_sf_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+
+// Unswizzled rows of 16 bytes: 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_rows16(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const uint32_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Arrive on a barrier of another CTA of the cluster, releasing this thread's
+// shared-memory writes to it.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void fence_acquire_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
+template <int FMT, int EPI>
+__device__ __forceinline__ void epilogue(const MxGemmArgs& a, const uint32_t (&v)[128],
+                                         const Tile& t, int r_in_tile, int half) {
+  if (r_in_tile >= t.rows) return;
+  const int row = t.row0 + r_in_tile;
+  if constexpr (EPI == MX_ROWS) {
+    const int dest = a.row_dest ? a.row_dest[row] : row;
+    if (dest < 0 || dest >= a.out_rows) return;
+    const float w = a.row_w ? a.row_w[row] : 1.0f;
+    const int col0 = t.nt * BN + half * 128;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      if (col0 + c < a.n_valid) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          pk[i] = pack_bf16x2(w * __uint_as_float(v[c + 2 * i]),
+                              w * __uint_as_float(v[c + 2 * i + 1]));
+        __nv_bfloat16* dst =
+            static_cast<__nv_bfloat16*>(a.out) + (size_t)dest * a.n_valid + col0 + c;
+        st_global_v8(dst, pk);
+        st_global_v8(dst + 16, pk + 8);
+      }
+    }
+  } else {
+    // gate in v[0..63], up in v[64..127]: two blocks of h, half a word of scales
+    const int col0 = t.nt * (BN / 2) + half * 64;
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (col0 + 32 * b < a.n_valid) {
+        float h[32];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          h[i] = silu_f(__uint_as_float(v[32 * b + i])) * __uint_as_float(v[64 + 32 * b + i]);
+          m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
+        }
+        const uint32_t byte = mx_scale_byte<FMT>(m);
+        bytes |= byte << (8 * b);
+        uint32_t q[8];
+        mx_encode<FMT>(h, byte, q);
+        uint8_t* dst = static_cast<uint8_t*>(a.out) +
+                       ((size_t)row * a.n_valid + col0 + 32 * b) / MxFmt<FMT>::kPerByte;
+        if constexpr (FMT == MOE_MXFP8)
+          st_global_v8(dst, q);
+        else
+          *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+    }
+    // the word's bytes past the last column's block are 0
+    uint16_t* s = reinterpret_cast<uint16_t*>(a.out_scales + (size_t)t.nt * a.rows + row);
+    s[half] = static_cast<uint16_t>(bytes);
+  }
+}
+
+template <int FMT, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    grouped_mx_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB, const MxGemmArgs args) {
+  using F = Fmt<FMT>;
+  pdl_launch_dependents();
+  pdl_wait();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem_sf = smem + (size_t)STAGES * STAGE_BYTES;
+  SmemTail& st = *reinterpret_cast<SmemTail*>(smem_sf + (size_t)STAGES * F::kSf);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+
+  // group table; offsets that run backwards or past the rows are cut to the
+  // rows, so that no access leaves the operands, and reported
+  if (threadIdx.x == 0) {
+    st.bad_offsets = 0;
+    if (blockIdx.x == 0 && args.clear_status) {
+      args.status[0] = 0;
+      args.status[1] = 0;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i <= args.groups; i += THREADS) {
+    const int o = args.offsets[i];
+    st.row_start[i] = min(max(o, 0), args.rows);
+    if (o < 0 || o > args.rows || (i > 0 && o < args.offsets[i - 1])) st.bad_offsets = 1;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&st.full[s], 1 + 4);  // leader: its producer, the scale warps of both CTAs
+      mbar_init(&st.empty[s], 1);     // both: one commit from the leader's MMA thread
+    }
+    mbar_init(&st.tfull, 1);
+    mbar_init(&st.tempty, 2 * EPI_WARPS);  // leader: every epilogue warp of both CTAs
+    mbar_init(&st.drain, 1);
+    st.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && blockIdx.x == 0 && st.bad_offsets)
+    report_error(args.status, MOE_ERR_DEVICE_INDEX, 60);
+  if (warp == 0) {  // exclusive prefix of tiles over groups (4 groups per lane)
+    constexpr int PER = MAX_GROUPS / 32;
+    int loc[PER], sum = 0;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int g = lane * PER + q;
+      loc[q] =
+          g < args.groups
+              ? (max(st.row_start[g + 1] - st.row_start[g], 0) + TILE_M - 1) / TILE_M
+              : 0;
+      sum += loc[q];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(FULL, incl, off);
+      if (lane >= off) incl += u;
+    }
+    int run = incl - sum;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int g = lane * PER + q;
+      if (g < args.groups) st.mt_start[g] = run;
+      run += loc[q];
+    }
+    if (lane == 31) st.mt_start[args.groups] = incl;
+  }
+  __syncthreads();
+  const int total = st.mt_start[args.groups] * args.n_tiles;
+  if (cluster >= total) return;  // the same for both CTAs of the cluster; nothing allocated yet
+  cluster_sync();                // both CTAs' barriers exist before any cross-CTA traffic
+
+  if (warp == 1) {
+    tmem_alloc_pair(&st.tmem_base, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = st.tmem_base;
+  const WaitCtx wc{&st.abort_flag, args.status, args.timeout_ns};
+  const int k_steps = (args.k_bytes + KB - 1) / KB;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------ TMA producer (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t armed = 0, armed_parity = 0;
+      bool ok = true;
+      for (int tile = cluster; ok && tile < total; tile += nclusters) {
+        const Tile t = tile_at(tile, args.n_tiles, args.groups, st.mt_start, st.row_start);
+        const int a_row = t.row0 + BM * (int)rank;
+        const int b_row = t.nt * args.n_out_tile + (int)rank * args.b_second;
+        const bool load_a = t.rows > BM * (int)rank;  // a half without rows loads none
+        const uint32_t tx = 2 * B_BYTES + A_BYTES + (t.rows > BM ? A_BYTES : 0);
+        for (int ks = 0; ks < k_steps; ++ks) {
+          if (!mbar_wait(&st.empty[stage], phase ^ 1u, wc, 61)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + (size_t)stage * STAGE_BYTES;
+          const uint32_t full_leader = mapa_shared(smem_u32(&st.full[stage]), 0);
+          if (leader) mbar_arrive_expect_tx(&st.full[stage], tx);
+          if (load_a) tma_load_2d_pair(sa, &tmA, full_leader, ks * KB, a_row);
+          tma_load_3d_pair(sa + A_BYTES, &tmB, full_leader, ks * KB, b_row, t.g);
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && leader) {  // both CTAs' loads are counted on the leader's barriers
+        for (int s = 0; s < STAGES; ++s)
+          if ((armed >> s) & 1u)
+            mbar_wait_drain(&st.full[s], (armed_parity >> s) & 1u, args.timeout_ns);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------ scales to TMEM and pair MMAs (leader)
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int tile = cluster; ok && tile < total; tile += nclusters) {
+        if (!mbar_wait(&st.tempty, acc_phase ^ 1u, wc, 62)) break;
+        tc_fence_after_sync();
+        for (int ks = 0; ks < k_steps; ++ks) {
+          if (!mbar_wait(&st.full[stage], phase, wc, 63)) {
+            ok = false;
+            break;
+          }
+          fence_acquire_cluster();  // the peer's scale words
+          tc_fence_after_sync();
+          const uint32_t sa = smem_u32(smem + (size_t)stage * STAGE_BYTES);
+          const uint32_t sf = smem_u32(smem_sf + (size_t)stage * F::kSf);
+          const uint32_t sfa = tmem_base + TMEM_SF + stage * TMEM_SF_STAGE;
+          const uint32_t sfb = sfa + TMEM_SFB;
+#pragma unroll
+          for (int w = 0; w < F::kWords; ++w) {
+            tmem_copy_sf_pair(sfa + 4 * w, sdesc_rows16(sf + w * SF_BYTES));
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+              tmem_copy_sf_pair(sfb + 8 * w + 4 * hb,
+                                sdesc_rows16(sf + (F::kWords + 2 * w + hb) * SF_BYTES));
+          }
+          const uint64_t da = sdesc_kmajor_sw128(sa);
+          const uint64_t db = sdesc_kmajor_sw128(sa + A_BYTES);
+          const int left = args.k_bytes - ks * KB;  // 32 bytes of every row per MMA
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk * 32 < left) {
+              const int w = kk * F::kWords / 4;  // the scale word, and the byte in it
+              const uint32_t id = FMT == MOE_MXFP8 ? kk : 2 * (kk & 1);
+              umma_mx_pair<FMT>(tmem_base, da + 2 * kk, db + 2 * kk, idesc_sf(idesc_mx<FMT>(), id),
+                                sfa + 4 * w, sfb + 8 * w, (ks | kk) != 0 ? 1u : 0u);
+            }
+          }
+          umma_commit_pair_mask(&st.empty[stage], 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair_mask(&st.tfull, 0x3);
+        acc_phase ^= 1u;
+      }
+      umma_commit_pair_mask(&st.drain, 0x1);  // all of this thread's MMAs are done
+      mbar_wait_drain(&st.drain, 0, args.timeout_ns);
+    }
+  } else if (warp < 10) {
+    // ------------------------------------------------ epilogue warps 2..9 (both CTAs)
+    const int q = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const int r_in_tile = q * 32 + lane;
+    const uint32_t tempty_leader = mapa_shared(smem_u32(&st.tempty), 0);
+    const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t acc_phase = 0;
+    for (int tile = cluster; tile < total; tile += nclusters) {
+      Tile t = tile_at(tile, args.n_tiles, args.groups, st.mt_start, st.row_start);
+      t.row0 += BM * (int)rank;
+      t.rows = max(0, min(BM, t.rows - BM * (int)rank));
+      const bool ok = mbar_wait(&st.tfull, acc_phase, wc, 64);
+      if (!__all_sync(FULL, ok)) break;  // warp-uniform exit
+      tc_fence_after_sync();
+      uint32_t v[128];
+      if constexpr (EPI == MX_SWIGLU) {
+        // accumulator columns [0,128) gate, [128,256) up; this half: 64 of each
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tmem_ld_32x32b_x32(tb + half * 64 + 32 * c,
+                             *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+          tmem_ld_32x32b_x32(tb + BN / 2 + half * 64 + 32 * c,
+                             *reinterpret_cast<uint32_t(*)[32]>(v + 64 + 32 * c));
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_ld_32x32b_x32(tb + half * 128 + 32 * c,
+                             *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+      }
+      tmem_ld_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(tempty_leader);
+      epilogue<FMT, EPI>(args, v, t, r_in_tile, half);
+      acc_phase ^= 1u;
+    }
+  } else {
+    // ------------------------------------------------ scale warps: A's rows, B's columns
+    const bool is_a = warp == 10;
+    const int words = args.words;
+    int stage = 0, done = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    auto arrive_oldest = [&]() {
+      fence_proxy_async_smem();  // cp.async writes -> tcgen05.cp reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&st.full[done % STAGES]), 0));
+      ++done;
+    };
+    for (int tile = cluster; ok && tile < total; tile += nclusters) {
+      const Tile t = tile_at(tile, args.n_tiles, args.groups, st.mt_start, st.row_start);
+      const int a_row0 = t.row0 + BM * (int)rank;
+      const int a_rows = min(BM, t.rows - BM * (int)rank);  // may be <= 0
+      for (int ks = 0; ks < k_steps; ++ks) {
+        const bool got = mbar_wait(&st.empty[stage], phase ^ 1u, wc, 65);
+        if (!__all_sync(FULL, got)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sf = smem_u32(smem_sf + (size_t)stage * F::kSf) + lane * 16;
+#pragma unroll
+        for (int w = 0; w < F::kWords; ++w) {
+          const int kw = ks * F::kWords + w;
+          if (kw < words) {
+            if (is_a) {
+              const uint32_t* src = args.a_scales + (size_t)kw * args.rows + a_row0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (lane + 32 * j < a_rows)
+                  cp_async_4(sf + w * SF_BYTES + 4 * j, src + lane + 32 * j);
+            } else {
+              const uint32_t* src =
+                  args.b_scales + ((size_t)t.g * words + kw) * args.n_rows;
+#pragma unroll
+              for (int hb = 0; hb < 2; ++hb) {
+                const int n0 = t.nt * args.n_out_tile + hb * args.b_second;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (n0 + lane + 32 * j < args.n_rows)
+                    cp_async_4(sf + (F::kWords + 2 * w + hb) * SF_BYTES + 4 * j,
+                               src + n0 + lane + 32 * j);
+              }
+            }
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++issued;
+        if (issued > SF_LAG) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(SF_LAG) : "memory");
+          arrive_oldest();
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    while (done < issued) arrive_oldest();
+  }
+
+  // both CTAs are done with the accumulator and the scales before either frees TMEM or exits
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Rows of bytes in boxes of 128 bytes x 128 rows, 128-byte swizzle; bytes past
+// a row's end and rows past a matrix's end read 0.
+cudaError_t make_tmap_bytes(CUtensorMap* map, const void* base, uint64_t groups, uint64_t rows,
+                            uint64_t row_bytes) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {row_bytes, rows, groups};
+  const cuuint64_t strides[2] = {row_bytes, rows * row_bytes};
+  const cuuint32_t box[3] = {KB, BM, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups ? 3 : 2, const_cast<void*>(base), dims,
+         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int FMT, int EPI>
+cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const MxGemmArgs& args,
+                   int grid, cudaStream_t stream) {
+  constexpr size_t smem = Fmt<FMT>::kSmem + sizeof(SmemTail);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static std::atomic<int> smem_set[MAX_DEVICES];
+  const cudaError_t e =
+      set_smem_limit_per_device(grouped_mx_kernel<FMT, EPI>, (int)smem, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_chained(grouped_mx_kernel<FMT, EPI>, dim3(grid), dim3(THREADS), smem, stream, tmA,
+                        tmB, args);
+}
+
+// Rows of narrow tokens in expert order: codes[r] = tokens[tok_of[r]] (16-byte
+// vectors) and the words of scales; a token outside [0, T) gives zeros.
+__global__ void __launch_bounds__(256)
+    gather_mx_kernel(const uint4* __restrict__ codes, const uint32_t* __restrict__ scales,
+                     const int* __restrict__ tok_of, int T, int R, int vecs, int words,
+                     uint4* __restrict__ codes_out, uint32_t* __restrict__ scales_out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long step = (long long)gridDim.x * blockDim.x;
+  const long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  for (long long i = i0; i < (long long)R * vecs; i += step) {
+    const int r = (int)(i / vecs);
+    const int c = (int)(i - (long long)r * vecs);
+    const int t = tok_of[r];
+    codes_out[i] = t >= 0 && t < T ? codes[(size_t)t * vecs + c] : make_uint4(0, 0, 0, 0);
+  }
+  for (long long i = i0; i < (long long)R * words; i += step) {
+    const int w = (int)(i / R);
+    const int r = (int)(i - (long long)w * R);
+    const int t = tok_of[r];
+    scales_out[i] = t >= 0 && t < T ? scales[(size_t)w * T + t] : 0u;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_mx(int fmt, int epi, const void* a, const void* b, MxGemmArgs args,
+                              cudaStream_t stream) {
+  if (args.groups > MAX_GROUPS) return cudaErrorInvalidValue;
+  CUtensorMap tmA, tmB;
+  cudaError_t e;
+  if ((e = make_tmap_bytes(&tmA, a, 0, args.rows, args.k_bytes)) != cudaSuccess) return e;
+  if ((e = make_tmap_bytes(&tmB, b, args.groups, args.n_rows, args.k_bytes)) != cudaSuccess)
+    return e;
+  args.n_out_tile = epi == MX_SWIGLU ? BN / 2 : BN;
+  args.n_tiles = (args.n_valid + args.n_out_tile - 1) / args.n_out_tile;
+  args.b_second = epi == MX_SWIGLU ? args.n_valid : BN / 2;
+  const long long tiles = ((long long)args.rows / TILE_M + args.groups) * args.n_tiles;
+  const int sms = num_sms() & ~1;
+  const int grid = (int)(2 * tiles < sms ? 2 * tiles : sms);
+  if (fmt == MOE_MXFP8)
+    return epi == MX_SWIGLU ? launch<MOE_MXFP8, MX_SWIGLU>(tmA, tmB, args, grid, stream)
+                            : launch<MOE_MXFP8, MX_ROWS>(tmA, tmB, args, grid, stream);
+  return epi == MX_SWIGLU ? launch<MOE_MXFP4, MX_SWIGLU>(tmA, tmB, args, grid, stream)
+                          : launch<MOE_MXFP4, MX_ROWS>(tmA, tmB, args, grid, stream);
+}
+
+cudaError_t launch_gather_mx(const uint8_t* codes, const uint8_t* scales, const int* tok_of, int T,
+                             int R, int row_bytes, int words, uint8_t* codes_out,
+                             uint8_t* scales_out, cudaStream_t stream) {
+  const int vecs = row_bytes / 16;
+  long long blocks = ((long long)R * vecs + 255) / 256;
+  const long long cap = (long long)num_sms() * 8;
+  if (blocks > cap) blocks = cap;
+  return launch_chained(gather_mx_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
+                        reinterpret_cast<const uint4*>(codes),
+                        reinterpret_cast<const uint32_t*>(scales), tok_of, T, R, vecs, words,
+                        reinterpret_cast<uint4*>(codes_out),
+                        reinterpret_cast<uint32_t*>(scales_out));
+}
+
+}  // namespace rmoe

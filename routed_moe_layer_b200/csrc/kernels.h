@@ -8,6 +8,8 @@
 #include <atomic>
 #include <utility>
 
+#include "routed_moe.h"
+
 namespace rmoe {
 
 // A kernel's dynamic shared-memory limit is an attribute of the kernel in one
@@ -188,6 +190,56 @@ cudaError_t launch_tile_prefix(const int* offsets, int groups, int* tiles, cudaS
 cudaError_t launch_combine_rows(const void* y, int R, const int* row_of, int top_k, int T, int H,
                                 const void* shared, const void* residual, void* out,
                                 cudaStream_t stream);
+
+// tile_prefix on offsets that a caller gave: start[g] (0..groups) the offsets cut to
+// [0, rows] and made non-decreasing, tiles as above; clears the status word, and leaves
+// MOE_ERR_DEVICE_INDEX in it when an offset had to be changed.
+cudaError_t launch_group_schedule(const int* offsets, int groups, int rows, int* start,
+                                  int* tiles, int* status, cudaStream_t stream);
+
+// ------------------------------------------------------------------ MX formats
+// Formats, rounding and storage: mx_format.cuh.
+inline int mx_words(int K) { return (K + 127) / 128; }  // scale words per row
+inline int mx_row_bytes(int K, int fmt) { return fmt == MOE_MXFP8 ? K : K / 2; }
+
+cudaError_t launch_mx_quantize(const void* x, int groups, int rows, int K, int fmt, uint8_t* codes,
+                               uint8_t* scales, cudaStream_t stream);
+cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int groups, int rows,
+                                 int K, int fmt, void* x, cudaStream_t stream);
+// fmt 0: no codes.  residual, gamma, sum, xn may be null.
+cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const float* gamma, float eps,
+                               int T, int H, int fmt, void* sum, void* xn, uint8_t* codes,
+                               uint8_t* scales, cudaStream_t stream);
+
+enum MxEpi { MX_ROWS = 0, MX_SWIGLU = 1 };
+
+struct MxGemmArgs {
+  const int* offsets;        // [groups+1] device: first row of each group
+  int groups;
+  int rows;                  // rows of A: no group reaches past them
+  const uint32_t* a_scales;  // [words][rows]
+  const uint32_t* b_scales;  // [groups][words][n_rows]
+  int n_rows;                // weight rows per group: N, or 2I (MX_SWIGLU)
+  int words;                 // scale words per row
+  int k_bytes;               // bytes per row of codes
+  int n_valid;               // output columns: N, or I (MX_SWIGLU)
+  const float* row_w;        // MX_ROWS: weight of each row, or null for 1
+  const int* row_dest;       // MX_ROWS: output row of each row, or null for the row itself
+  int out_rows;              // MX_ROWS: rows of out; a destination outside is not stored
+  void* out;                 // bf16 [out_rows, N], or codes [rows, I]
+  uint32_t* out_scales;      // MX_SWIGLU: [mx_words(I)][rows]
+  int* status;
+  int clear_status;          // 1: the status word is cleared first
+  unsigned long long timeout_ns;
+  int n_tiles, n_out_tile, b_second;  // set by launch_grouped_mx
+};
+
+// a: codes [rows, k_bytes]; b: codes [groups, n_rows, k_bytes].
+cudaError_t launch_grouped_mx(int fmt, int epi, const void* a, const void* b, MxGemmArgs args,
+                              cudaStream_t stream);
+cudaError_t launch_gather_mx(const uint8_t* codes, const uint8_t* scales, const int* tok_of, int T,
+                             int R, int row_bytes, int words, uint8_t* codes_out,
+                             uint8_t* scales_out, cudaStream_t stream);
 
 // ------------------------------------------------------------------ misc
 cudaError_t launch_rmsnorm(const void* x, const float* gamma, float eps, int T, int H, void* xn,

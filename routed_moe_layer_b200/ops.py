@@ -24,6 +24,7 @@ STATUS_NAMES = {
     3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE_TIMEOUT",
     6: "MOE_ERR_DEVICE_INDEX", 7: "MOE_ERR_NO_DEVICE",
 }
+MX_FORMATS = {"mxfp8": 1, "mxfp4": 2}  # moe_mx_format_t
 STAGES = ("router", "permute", "expert_up", "expert_down", "shared_expert", "combine")
 NUM_STAGES = len(STAGES)
 
@@ -107,6 +108,17 @@ def lib() -> ctypes.CDLL:
         "moe_expert_rows": (i32, [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
         "moe_combine_rows": (i32, [vp, i32, vp, i32, i32, i32, vp, vp, vp, vp]),
         "moe_rmsnorm": (i32, [vp, vp, ctypes.c_float, i32, i32, vp, vp]),
+        "moe_mx_quantize": (i32, [vp, i32, i32, i32, i32, vp, vp, vp]),
+        "moe_mx_dequantize": (i32, [vp, vp, i32, i32, i32, i32, vp, vp]),
+        "moe_add_rmsnorm": (i32, [vp, vp, vp, ctypes.c_float, i32, i32, i32, vp, vp, vp, vp, vp]),
+        "moe_grouped_mm_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "moe_grouped_mm_mx_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "moe_grouped_mm": (i32, [vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]),
+        "moe_grouped_mm_mx": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32,
+                                    vp, sz, vp]),
+        "moe_expert_rows_mx_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
+        "moe_expert_rows_mx": (i32, [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp,
+                                     vp, vp, vp, i32, vp, sz, vp]),
         "moe_read_device_status": (i32, [vp, ctypes.POINTER(i32), vp]),
         "moe_selftest_wait_timeout": (i32, [vp, i64, vp]),
     }
@@ -506,6 +518,223 @@ def rmsnorm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, eps: float = 
     _check(lib().moe_rmsnorm(_ptr(x), _ptr(gamma), float(eps), T, H, _ptr(out), _stream_ptr()),
            "moe_rmsnorm")
     return out
+
+
+# ---------------------------------------------------------------- narrow formats (MX)
+# Codes and scales as moe_mx_quantize lays them out (include/routed_moe.h): codes uint8
+# [rows, K] ("mxfp8") or [rows, K/2] ("mxfp4"), scales uint8 [ceil(K/128), rows, 4]; a stack of
+# matrices has one more leading dimension in both.  These calls run on the device of their
+# tensors, on that device's current stream.
+
+def _fmt(fmt: str) -> int:
+    if fmt not in MX_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}, got {fmt!r}")
+    return MX_FORMATS[fmt]
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
+    return first.device
+
+
+def _call(name: str, dev: torch.device, *args):
+    """Calls entry point ``name`` with dev current, on dev's current stream."""
+    fn = getattr(lib(), name)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, stream), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream), name)
+
+
+def mx_words(K: int) -> int:
+    """Scale words (four blocks of 32 elements) of a row of K elements."""
+    return (K + 127) // 128
+
+
+def _need_mx(codes: torch.Tensor, scales: torch.Tensor, name: str, lead: Sequence[int], rows: int,
+             K: int, fmt: int):
+    _need(codes, f"{name}_codes", torch.uint8, (*lead, rows, K if fmt == 1 else K // 2))
+    _need(scales, f"{name}_scales", torch.uint8, (*lead, mx_words(K), rows, 4))
+
+
+def _matrices(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a matrix or a stack of matrices")
+    return (t.shape[0] if t.dim() == 3 else 1), tuple(t.shape[:-2]), t.shape[-2], t.shape[-1]
+
+
+def mx_quantize(x: torch.Tensor, fmt: str):
+    """(codes, scales) of bf16 x [rows, K] or [G, rows, K] (moe_mx_quantize)."""
+    f = _fmt(fmt)
+    G, lead, rows, K = _matrices(x, "x")
+    _need(x, "x", torch.bfloat16, (*lead, rows, K))
+    codes = torch.empty((*lead, rows, K if f == 1 else K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*lead, mx_words(K), rows, 4), dtype=torch.uint8, device=x.device)
+    _call("moe_mx_quantize", x.device, x.data_ptr(), G, rows, K, f, codes.data_ptr(),
+          scales.data_ptr())
+    return codes, scales
+
+
+def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: str) -> torch.Tensor:
+    """bf16 values of (codes, scales) (moe_mx_dequantize)."""
+    f = _fmt(fmt)
+    G, lead, rows, K = _matrices(codes, "codes")
+    K = K if f == 1 else 2 * K
+    _need_mx(codes, scales, "x", lead, rows, K, f)
+    dev = _one_device(codes, scales)
+    x = torch.empty((*lead, rows, K), dtype=torch.bfloat16, device=dev)
+    _call("moe_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), G, rows, K, f,
+          x.data_ptr())
+    return x
+
+
+def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                fmt: Optional[str] = None, sum_out: Optional[torch.Tensor] = None):
+    """RMSNorm of x + residual (moe_add_rmsnorm): returns (sum, xn), and with
+    ``fmt`` (sum, xn, codes, scales), the MX form of xn.  ``sum_out`` receives
+    the sum (x or residual: in place); without a residual the sum is x."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    T, H = x.shape
+    _need(x, "x", torch.bfloat16, (T, H))
+    f = 0 if fmt is None else _fmt(fmt)
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (T, H))
+    if gamma is not None:
+        _need(gamma, "gamma", torch.float32, (H,))
+    if sum_out is not None:
+        _need(sum_out, "sum_out", torch.bfloat16, (T, H))
+    dev = _one_device(x, residual, gamma, sum_out)
+    total = sum_out
+    if total is None:
+        total = x if residual is None else torch.empty_like(x)
+    xn = torch.empty_like(x)
+    codes = scales = None
+    if f:
+        codes = torch.empty((T, H if f == 1 else H // 2), dtype=torch.uint8, device=dev)
+        scales = torch.empty((mx_words(H), T, 4), dtype=torch.uint8, device=dev)
+    _call("moe_add_rmsnorm", dev, x.data_ptr(), _at(residual), _at(gamma), float(eps), T, H, f,
+          None if total is x and residual is None else total.data_ptr(), xn.data_ptr(),
+          _at(codes), _at(scales))
+    return (total, xn) if f == 0 else (total, xn, codes, scales)
+
+
+def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+               out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows grouped by expert times their expert's matrix (moe_grouped_mm): bf16
+    x [R,K], w [E,N,K], int32 offsets [E+1] -> bf16 [R,N].  Rows outside the
+    groups keep what ``out`` holds (undefined without ``out``)."""
+    if not (isinstance(x, torch.Tensor) and isinstance(w, torch.Tensor)):
+        raise TypeError("x and w must be tensors")
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be a matrix and w a stack of matrices")
+    R, K = x.shape
+    E, N, _ = w.shape
+    _need(x, "x", torch.bfloat16, (R, K))
+    _need(w, "w", torch.bfloat16, (E, N, K))
+    _need(offsets, "offsets", torch.int32, (E + 1,))
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, "out", torch.bfloat16, (R, N))
+    dev = _one_device(x, w, offsets, out, workspace)
+    if workspace is None:
+        workspace = alloc_workspace(lib().moe_grouped_mm_workspace_bytes(R, E, N, K), dev)
+    _call("moe_grouped_mm", dev, x.data_ptr(), offsets.data_ptr(), R, E, N, K, w.data_ptr(),
+          out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def _mx_out(R: int, N: int, dev, row_w, row_dest, out, out_rows):
+    if row_w is not None:
+        _need(row_w, "row_w", torch.float32, (R,))
+    if row_dest is not None:
+        _need(row_dest, "row_dest", torch.int32, (R,))
+    if out is None:
+        return torch.empty((R if out_rows is None else out_rows, N), dtype=torch.bfloat16,
+                           device=dev)
+    if out_rows is None:
+        out_rows = out.shape[0] if isinstance(out, torch.Tensor) and out.dim() == 2 else R
+    _need(out, "out", torch.bfloat16, (out_rows, N))
+    return out
+
+
+def grouped_mm_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
+                  w_scales: torch.Tensor, offsets: torch.Tensor, fmt: str,
+                  row_w: Optional[torch.Tensor] = None, row_dest: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, out_rows: Optional[int] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """grouped_mm of MX operands (moe_grouped_mm_mx): rows (x_codes, x_scales) of
+    K elements, E matrices (w_codes, w_scales) [E,N,K] -> bf16 [out_rows
+    (default R), N], row r weighted by row_w[r] and stored at row_dest[r]."""
+    f = _fmt(fmt)
+    _, xl, R, kb = _matrices(x_codes, "x_codes")
+    E, wl, N, _ = _matrices(w_codes, "w_codes")
+    if xl or not wl:
+        raise ValueError("x must be a matrix and w a stack of matrices")
+    K = kb if f == 1 else 2 * kb
+    _need_mx(x_codes, x_scales, "x", (), R, K, f)
+    _need_mx(w_codes, w_scales, "w", (E,), N, K, f)
+    _need(offsets, "offsets", torch.int32, (E + 1,))
+    y = _mx_out(R, N, x_codes.device, row_w, row_dest, out, out_rows)
+    dev = _one_device(x_codes, x_scales, w_codes, w_scales, offsets, row_w, row_dest, y, workspace)
+    if workspace is None:
+        workspace = alloc_workspace(256, dev)
+    _call("moe_grouped_mm_mx", dev, x_codes.data_ptr(), x_scales.data_ptr(), offsets.data_ptr(), R,
+          E, N, K, f, w_codes.data_ptr(), w_scales.data_ptr(), _at(row_w), _at(row_dest),
+          y.data_ptr(), y.shape[0], workspace.data_ptr(), workspace.numel())
+    return y
+
+
+def expert_rows_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor,
+                   w13_codes: torch.Tensor, w13_scales: torch.Tensor, w2_codes: torch.Tensor,
+                   w2_scales: torch.Tensor, row_dest: Optional[torch.Tensor], fmt: str,
+                   row_w: Optional[torch.Tensor] = None, tok_of: Optional[torch.Tensor] = None,
+                   y: Optional[torch.Tensor] = None, y_rows: Optional[int] = None,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Routed experts on MX rows and weights (moe_expert_rows_mx), the narrow form
+    of expert_rows.  (x_codes, x_scales): tokens, gathered through tok_of [R], or
+    (tok_of None) the rows already grouped; w13 [E,2I,H], w2 [E,H,I].  Returns y
+    bf16 [y_rows (default R), H]."""
+    f = _fmt(fmt)
+    _, xl, T, hb = _matrices(x_codes, "x_codes")
+    E, wl, I2, _ = _matrices(w13_codes, "w13_codes")
+    if xl or not wl:
+        raise ValueError("x must be a matrix and w13, w2 stacks of matrices")
+    H, I = (hb if f == 1 else 2 * hb), I2 // 2
+    _need_mx(x_codes, x_scales, "x", (), T, H, f)
+    _need_mx(w13_codes, w13_scales, "w13", (E,), 2 * I, H, f)
+    _need_mx(w2_codes, w2_scales, "w2", (E,), H, I, f)
+    _need(offsets, "offsets", torch.int32, (E + 1,))
+    R = T
+    if tok_of is not None:
+        R = tok_of.numel()
+        _need(tok_of, "tok_of", torch.int32, (R,))
+    y = _mx_out(R, H, x_codes.device, row_w, row_dest, y, y_rows)
+    dev = _one_device(x_codes, x_scales, offsets, w13_codes, w13_scales, w2_codes, w2_scales,
+                      row_dest, row_w, tok_of, y, workspace)
+    if workspace is None:
+        workspace = alloc_workspace(lib().moe_expert_rows_mx_workspace_bytes(
+            R, H, E, I, f, int(tok_of is not None)), dev)
+    _call("moe_expert_rows_mx", dev, x_codes.data_ptr(), x_scales.data_ptr(), T, _at(tok_of),
+          offsets.data_ptr(), R, E, H, I, f, w13_codes.data_ptr(), w13_scales.data_ptr(),
+          w2_codes.data_ptr(), w2_scales.data_ptr(), _at(row_w), _at(row_dest), y.data_ptr(),
+          y.shape[0], workspace.data_ptr(), workspace.numel())
+    return y
 
 
 def read_device_status(workspace: torch.Tensor):

@@ -1,0 +1,410 @@
+"""The narrow-format operators on a B200 against the float64 oracle.
+
+Quantisation, its inverse and the norm's codes are compared bit for bit.  A
+product's output is held to its own rounding, 2^-8 of the value (bf16, to
+nearest), plus the fp32 accumulation: the products of two elements are exact
+in fp32 (at most 8 bits of mantissa; bf16 products: 16), and every one of K additions
+loses at most 2^-23 of the sum of magnitudes S (truncation allowed): K * 2^-23 * S."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import bf16_round, mx_oracle as mx
+from routed_moe_layer_b200 import ops
+from tests.parity import to_np
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+FMTS = ["mxfp8", "mxfp4"]
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def values(rows, K, seed):
+    """bf16 rows of different sizes, with zeros, ties, subnormals and large values."""
+    g = gen(seed)
+    x = torch.randn(rows, K, generator=g) * torch.exp(2 * torch.randn(rows, 1, generator=g))
+    x = x.bfloat16().float()
+    flat = x.view(-1)
+    special = torch.tensor([0.0, -0.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 448.0, 17.0,
+                            2.0 ** -130, -2.0 ** -133, 3e38, -3e38, 1.1875, 1.0625])
+    at = torch.randint(0, flat.numel(), (max(1, flat.numel() // 40),), generator=g)
+    flat[at] = special[torch.randint(0, len(special), (len(at),), generator=g)]
+    return x.bfloat16()
+
+
+def stored(codes, scales, fmt):
+    c, s = mx.mx_store(codes, scales, fmt)
+    return torch.from_numpy(c), torch.from_numpy(s)
+
+
+def operands(rows, K, fmt, seed, lead=None, scale=1.0):
+    """Random MX operands made by the oracle: device arrays and their float64 values."""
+    g = gen(seed)
+    n = rows if lead is None else lead * rows
+    x = (scale * torch.randn(n, K, generator=g) * torch.exp(torch.randn(n, 1, generator=g))).numpy()
+    codes, scales = fast_quantize(x, fmt)
+    v = mx.mx_values(codes, scales, fmt)
+    if lead is None:
+        c, s = stored(codes, scales, fmt)
+        return c.to(DEV), s.to(DEV), v
+    parts = [stored(codes[i * rows:(i + 1) * rows], scales[i * rows:(i + 1) * rows], fmt)
+             for i in range(lead)]
+    return (torch.stack([p[0] for p in parts]).to(DEV), torch.stack([p[1] for p in parts]).to(DEV),
+            v.reshape(lead, rows, K))
+
+
+def fast_quantize(x, fmt):
+    """The oracle's quantisation, blocks at once (finite values)."""
+    b = x.astype(np.float64).reshape(x.shape[0], -1, 32)
+    amax = np.abs(b).max(2)
+    p = np.vectorize(lambda a: mx.mx_power(a, fmt))(amax) if amax.size else np.zeros(amax.shape, int)
+    codes = mx.mx_round(b / (2.0 ** p)[:, :, None], fmt).reshape(x.shape)
+    return codes, (p + 127).astype(np.uint8)
+
+
+def groups(R, E, seed, lead_rows=0, tail_rows=0):
+    """Ragged offsets over R rows: some groups empty, rows before and after the groups."""
+    g = np.random.default_rng(seed)
+    cuts = np.sort(g.integers(lead_rows, R - tail_rows + 1, E - 1)) if E > 1 else np.zeros(0, int)
+    return np.concatenate([[lead_rows], cuts, [R - tail_rows]]).astype(np.int32)
+
+
+def check_product(y, x, w, off, row_w=None, dest=None):
+    ref = mx.grouped_mm(x, w, off)
+    S = mx.grouped_mm(np.abs(x), np.abs(w), off)
+    K = x.shape[1]
+    if row_w is not None:
+        ref, S = ref * row_w[:, None], S * np.abs(row_w)[:, None]
+    got = to_np(y).astype(np.float64)
+    if dest is not None:
+        got = got[dest]
+    rows = slice(off[0], off[-1])
+    # one more fp32 rounding for the row weight
+    tol = 2.0 ** -8 * np.abs(ref) + (K + 2) * 2.0 ** -23 * S
+    err = np.abs(got - ref)[rows]
+    assert np.all(err <= tol[rows] * (1 + 1e-6)), (np.max(err / np.maximum(tol[rows], 1e-300)))
+
+
+# ------------------------------------------------------------------ quantisation
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,K", [(1, 32), (3, 96), (5, 128), (33, 160), (257, 224), (64, 1024),
+                                    (2, 16384)])
+def test_quantize_is_the_oracles(rows, K, fmt):
+    x = values(rows, K, rows * 1000 + K)
+    want_c, want_s = stored(*mx.mx_quantize(to_np(x), fmt), fmt)
+    c, s = ops.mx_quantize(x.to(DEV), fmt)
+    assert torch.equal(s.cpu(), want_s)
+    assert torch.equal(c.cpu(), want_c)
+    back = ops.mx_dequantize(c, s, fmt)
+    v = mx.mx_values(*mx.mx_load(c.cpu().numpy(), s.cpu().numpy(), K, fmt), fmt)
+    assert np.array_equal(to_np(back), bf16_round(v))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_every_bf16_value(fmt):
+    """Each of the 65,536 bf16 patterns alone in its block (zeros beside it), and
+    beside a 1.0: every scale byte, subnormals, infinities, NaN."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = torch.zeros(65536, 64, dtype=torch.bfloat16)
+    x[:, 5] = bits
+    x[:, 40] = bits
+    x[:, 41] = 1.0
+    c, s = ops.mx_quantize(x.to(DEV), fmt)
+    xn = x.double().numpy()
+    finite = np.isfinite(xn).all(1)
+    codes, scales = np.zeros(x.shape, np.uint8), np.full((65536, 2), 255, np.uint8)
+    codes[finite], scales[finite] = fast_quantize(xn[finite], fmt)
+    want_c, want_s = stored(codes, scales, fmt)
+    assert torch.equal(s.cpu(), want_s)
+    assert torch.equal(c.cpu(), want_c)
+    back = to_np(ops.mx_dequantize(c, s, fmt))
+    assert np.array_equal(np.isnan(back).any(1), ~finite)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_stack_is_its_matrices(fmt):
+    x = torch.stack([values(33, 96, 7), values(33, 96, 8), values(33, 96, 9)]).to(DEV)
+    c, s = ops.mx_quantize(x, fmt)
+    assert s.shape == (3, 1, 33, 4)
+    for i in range(3):
+        ci, si = ops.mx_quantize(x[i].contiguous(), fmt)
+        assert torch.equal(c[i], ci) and torch.equal(s[i], si)
+    assert torch.equal(ops.mx_dequantize(c, s, fmt)[1], ops.mx_dequantize(c[1], s[1], fmt))
+
+
+def test_quantize_offsets_past_32_bits():
+    rows, K = 140000, 16384  # 2.29e9 elements
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)
+    x[rows - 1] = values(1, K, 3)[0].to(DEV)
+    c, s = ops.mx_quantize(x, "mxfp8")
+    c1, s1 = ops.mx_quantize(x[rows - 1:].contiguous(), "mxfp8")
+    assert torch.equal(c[rows - 1:], c1) and torch.equal(s[:, rows - 1:], s1)
+    assert not c[rows - 2].any()
+    del x
+    assert torch.equal(ops.mx_dequantize(c, s, "mxfp8")[rows - 1:], ops.mx_dequantize(c1, s1, "mxfp8"))
+
+
+def test_empty_and_misaligned_calls():
+    c, s = ops.mx_quantize(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV), "mxfp4")
+    assert c.shape == (0, 32) and s.shape == (1, 0, 4)
+    buf = torch.zeros(4 * 64 + 8, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):
+        ops.mx_quantize(buf[4:4 + 256].view(4, 64), "mxfp8")  # 8 bytes off
+    with pytest.raises(ValueError, match="contiguous"):
+        ops.mx_quantize(torch.zeros(64, 64, dtype=torch.bfloat16, device=DEV).t(), "mxfp8")
+
+
+# ------------------------------------------------------------------ norm
+@pytest.mark.parametrize("fmt", [None] + FMTS)
+@pytest.mark.parametrize("T,H", [(1, 64), (3, 192), (17, 1024), (5, 1088), (300, 2048), (9, 4096),
+                                 (2, 8192), (3, 16384)])
+def test_add_rmsnorm(T, H, fmt):
+    g = gen(T + H)
+    x = torch.randn(T, H, generator=g).bfloat16()
+    r = (3 * torch.randn(T, H, generator=g)).bfloat16()
+    x[T // 2] = 0
+    r[T // 2] = 0  # an all-zero row
+    gamma = 1 + 0.2 * torch.randn(H, generator=g)
+    for res, gm, eps in ((r, gamma, 1e-6), (None, None, 1e-5), (r, None, 0.1)):
+        ref_s, ref = mx.add_rmsnorm(to_np(x), None if res is None else to_np(res), eps,
+                                    None if gm is None else gm.numpy())
+        d = [None if t is None else t.to(DEV) for t in (x, res, gm)]
+        out = ops.add_rmsnorm(d[0], d[1], d[2], eps=eps, fmt=fmt)
+        assert np.array_equal(to_np(out[0]), ref_s)
+        # half a bf16 step, and in fp32: the sum of squares loses at most H * 2^-24 of itself
+        # (half of that after the root), the quotient, root and two products half a step each
+        tol = (2.0 ** -8 + (H / 2 + 6) * 2.0 ** -24) * np.abs(ref)
+        assert np.all(np.abs(to_np(out[1]) - ref) <= tol * (1 + 1e-6) + 1e-40)
+        if fmt:
+            c, s = ops.mx_quantize(out[1], fmt)
+            assert torch.equal(out[2], c) and torch.equal(out[3], s)
+
+
+@pytest.mark.parametrize("which", ["x", "residual"])
+def test_add_rmsnorm_in_place(which):
+    g = gen(5)
+    x, r = torch.randn(40, 640, generator=g).bfloat16().to(DEV), torch.randn(40, 640, generator=g).bfloat16().to(DEV)
+    want = ops.add_rmsnorm(x, r, fmt="mxfp8")
+    a, b = x.clone(), r.clone()
+    got = ops.add_rmsnorm(a, b, fmt="mxfp8", sum_out=a if which == "x" else b)
+    assert got[0].data_ptr() == (a if which == "x" else b).data_ptr()
+    for u, v in zip(want, got):
+        assert torch.equal(u, v)
+    assert torch.equal(b if which == "x" else a, r if which == "x" else x)
+    # a row alone gives the row's bits in the batch
+    one = ops.add_rmsnorm(x[7:8], r[7:8], fmt="mxfp8")
+    assert torch.equal(one[1], want[1][7:8]) and torch.equal(one[2], want[2][7:8])
+    assert torch.equal(one[3][:, 0], want[3][:, 7])
+
+
+def test_add_rmsnorm_propagates_nan_to_its_row_alone():
+    x = torch.ones(4, 128, dtype=torch.bfloat16, device=DEV)
+    x[2, 77] = float("nan")
+    _, xn, c, s = ops.add_rmsnorm(x, fmt="mxfp4")
+    assert torch.isnan(xn[2]).all() and not torch.isnan(xn[[0, 1, 3]]).any()
+    assert (s[:, 2] == 255).all() and (s[:, [0, 1, 3]] != 255).all()
+
+
+# ------------------------------------------------------------------ products
+SHAPES = [  # R, E, N, K
+    (1, 1, 32, 32), (8, 16, 64, 96), (40, 3, 96, 160), (257, 5, 160, 352), (300, 2, 544, 512),
+    (600, 1, 256, 128), (1000, 7, 288, 1056), (515, 128, 64, 256),
+]
+
+
+@pytest.mark.parametrize("R,E,N,K", SHAPES)
+def test_grouped_mm(R, E, N, K):
+    g = gen(R + N)
+    x = torch.randn(R, K, generator=g).bfloat16()
+    w = torch.randn(E, N, K, generator=g).bfloat16()
+    lead, tail = (2, 3) if R > 30 else (0, 0)
+    off = groups(R, E, R, lead, tail)
+    out = torch.full((R, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = ops.alloc_workspace(4096, DEV)
+    y = ops.grouped_mm(x.to(DEV), w.to(DEV), torch.from_numpy(off).to(DEV), out=out, workspace=ws)
+    assert ops.read_device_status(ws)[0] == 0
+    check_product(y, to_np(x), to_np(w), off)
+    assert (y[:lead] == 7).all() and (y[R - tail:] == 7).all()  # rows outside the groups
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R,E,N,K", SHAPES)
+def test_grouped_mm_mx(R, E, N, K, fmt):
+    xc, xs, x = operands(R, K, fmt, R + K)
+    wc, wsc, w = operands(N, K, fmt, N + K, lead=E, scale=0.1)
+    lead, tail = (2, 3) if R > 30 else (0, 0)
+    off = groups(R, E, R, lead, tail)
+    out = torch.full((R, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = ops.alloc_workspace(256, DEV)
+    y = ops.grouped_mm_mx(xc, xs, wc, wsc, torch.from_numpy(off).to(DEV), fmt, out=out, workspace=ws)
+    assert ops.read_device_status(ws)[0] == 0
+    check_product(y, x, w, off)
+    assert (y[:lead] == 7).all() and (y[R - tail:] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_grouped_mm_mx_weights_and_destinations(fmt):
+    R, E, N, K, rows = 300, 6, 128, 256, 350
+    xc, xs, x = operands(R, K, fmt, 1)
+    wc, wsc, w = operands(N, K, fmt, 2, lead=E)
+    off = groups(R, E, 4)
+    g = gen(9)
+    row_w = torch.randn(R, generator=g)
+    dest = torch.randperm(rows, generator=g)[:R].int()
+    dest[10], dest[20] = -1, rows  # not stored
+    out = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ops.grouped_mm_mx(xc, xs, wc, wsc, torch.from_numpy(off).to(DEV), fmt, row_w=row_w.to(DEV),
+                      row_dest=dest.to(DEV), out=out)
+    kept = np.ones(R, bool)
+    kept[[10, 20]] = False
+    ref, S = mx.grouped_mm(x, w, off), mx.grouped_mm(np.abs(x), np.abs(w), off)
+    rw = row_w.numpy().astype(np.float64)[:, None]
+    got = to_np(out)[dest.numpy()[kept]]
+    tol = 2.0 ** -8 * np.abs(ref * rw) + (K + 2) * 2.0 ** -23 * S * np.abs(rw)
+    assert np.all(np.abs(got - (ref * rw)[kept]) <= tol[kept] * (1 + 1e-6))
+    free = np.setdiff1d(np.arange(rows), dest.numpy()[kept])
+    assert (out[torch.from_numpy(free).to(DEV)] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_every_element_and_scale_reaches_the_product(fmt):
+    """One-hot rows against matrices of every code: the product reads each
+    element, each row's and each column's scale from the right place."""
+    K, N = 512, 256
+    grid = mx.mx_grid(fmt)
+    n = 2 * len(grid)
+    signed = np.array([c if c < len(grid) else c - len(grid) + (128 if fmt == "mxfp8" else 8)
+                       for c in range(n)], np.uint8)
+    rng = np.random.default_rng(3)
+    wc = signed[rng.integers(0, n, (N, K))]
+    wsb = rng.integers(117, 137, (N, K // 32)).astype(np.uint8)
+    xc = np.zeros((K, K), np.uint8)
+    one = 0x38 if fmt == "mxfp8" else 2  # 1.0
+    xc[np.arange(K), np.arange(K)] = one
+    xsb = rng.integers(117, 137, (K, K // 32)).astype(np.uint8)
+    xd, xsd = stored(xc, xsb, fmt)
+    wd, wsd = stored(wc, wsb, fmt)
+    off = torch.tensor([0, K], dtype=torch.int32, device=DEV)
+    y = ops.grouped_mm_mx(xd.to(DEV), xsd.to(DEV), wd[None].to(DEV), wsd[None].to(DEV), off, fmt)
+    ref = mx.mx_values(xc, xsb, fmt) @ mx.mx_values(wc, wsb, fmt).T  # one term each: exact
+    assert np.array_equal(to_np(y), ref)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_nan_blocks_reach_their_rows_and_columns_alone(fmt):
+    R, N, K = 200, 96, 160
+    xc, xs, _ = operands(R, K, fmt, 3)
+    wc, wsc, _ = operands(N, K, fmt, 4, lead=1)
+    xs[1, 150, 0] = 255   # block 4 of row 150
+    wsc[0, 0, 17, 2] = 255
+    y = ops.grouped_mm_mx(xc, xs, wc, wsc, torch.tensor([0, R], dtype=torch.int32, device=DEV), fmt)
+    nan = torch.isnan(y)
+    assert nan[150].all() and nan[:, 17].all()
+    nan[150] = False
+    nan[:, 17] = False
+    assert not nan.any()
+
+
+def test_bad_offsets_are_reported_and_write_nothing_outside():
+    R, E, N, K = 600, 4, 64, 64
+    x = torch.ones(R, K, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(E, N, K, dtype=torch.bfloat16, device=DEV)
+    xc, xs = ops.mx_quantize(x, "mxfp8")
+    wc, wsc = ops.mx_quantize(w, "mxfp8")
+    buf = torch.full((R + 64, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = ops.alloc_workspace(4096, DEV)
+    for bad in ([0, 100, 300, 500, R + 50], [-5, 10, 20, 30, 40], [0, 400, 200, 500, 600],
+                [2 ** 30, 2 ** 31 - 1, 5, 6, 7]):
+        off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        ops.grouped_mm(x, w, off, out=buf[:R], workspace=ws)
+        assert ops.read_device_status(ws)[0] == 6
+        ops.grouped_mm_mx(xc, xs, wc, wsc, off, "mxfp8", out=buf[:R], workspace=ws)
+        assert ops.read_device_status(ws)[0] == 6
+        assert (buf[R:] == 7).all()
+    ok = torch.tensor([0, 100, 100, 500, R], dtype=torch.int32, device=DEV)
+    ops.grouped_mm(x, w, ok, out=buf[:R], workspace=ws)
+    assert ops.read_device_status(ws)[0] == 0  # cleared by the next call
+    assert (buf[:R] == K).all()
+
+
+# ------------------------------------------------------------------ experts
+def experts_tolerance(x, w13, w2, off, fmt, row_w):
+    """ref and the bound of |y - ref|: h's fp32 errors move an element over a
+    rounding border only where it lies that near to one; each such element may be
+    one step of its grid off (its block's power too, where the block's largest
+    element lies that near to the power's border)."""
+    H, I = x.shape[1], w13.shape[1] // 2
+    gu, S = mx.grouped_mm(x, w13, off), mx.grouped_mm(np.abs(x), np.abs(w13), off)
+    h = mx.swiglu(gu)
+    g, u = gu[:, :I], gu[:, I:]
+    eg, eu = H * 2.0 ** -23 * S[:, :I], H * 2.0 ** -23 * S[:, I:]
+    silu = g / (1 + np.exp(-g))
+    # silu' lies within +-1.1; its fast exponential and divide are within 2^-19 of it
+    d = 1.1 * eg * np.abs(u) + (np.abs(silu) + 1.1 * eg) * eu + 2.0 ** -19 * np.abs(h)
+    codes, scales = fast_quantize(h, fmt)
+    q = mx.mx_values(codes, scales, fmt)
+    lo, hi = nearest(h - d, h, fmt), nearest(h + d, h, fmt)
+    slack = np.maximum(np.abs(lo - q), np.abs(hi - q))
+    b = np.abs(h).reshape(len(h), -1, 32)
+    top = mx.mx_grid(fmt)[-1] * 2.0 ** (scales.astype(int) - 127)
+    amax, dm = b.max(2), d.reshape(b.shape).max(2)
+    border = (amax + dm > top) | (amax - dm <= top / 2)
+    # the whole block may then lie on the neighbouring power's grid: at most one step of the
+    # wider one at its largest element (E4M3 2^-3, E2M1 1/2 of the element's binade, doubled)
+    step = (0.25 if fmt == "mxfp8" else 1.0) * 2 * amax
+    slack = np.maximum(slack, np.repeat(np.where(border, step, 0.0), 32, axis=1))
+    ref = mx.grouped_mm(q, w2, off) * row_w[:, None]
+    Sh = mx.grouped_mm(np.abs(q) + slack, np.abs(w2), off)
+    tol = mx.grouped_mm(slack, np.abs(w2), off) + (I + 2) * 2.0 ** -23 * Sh
+    tol = tol * np.abs(row_w)[:, None]
+    return ref, tol + 2.0 ** -8 * (np.abs(ref) + tol)
+
+
+def nearest(v, like, fmt):
+    """v rounded on the grids (powers) that ``like`` has, saturated there."""
+    _, scales = fast_quantize(like, fmt)
+    p = np.repeat(2.0 ** (scales.astype(float) - 127), 32, axis=1)
+    top = mx.mx_grid(fmt)[-1]
+    codes = mx.mx_round(np.clip(v / p, -top, top), fmt)
+    return mx.mx_values(codes, scales, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 4, 64, 32), (9, 4, 2, 160, 96), (70, 16, 4, 256, 160),
+                                       (400, 3, 2, 512, 288), (333, 1, 1, 96, 128)])
+def test_expert_rows_mx(T, E, k, H, I, fmt):
+    xc, xs, x = operands(T, H, fmt, T + H)
+    w13c, w13s, w13 = operands(2 * I, H, fmt, H + I, lead=E, scale=H ** -0.5)
+    w2c, w2s, w2 = operands(H, I, fmt, I, lead=E, scale=I ** -0.5)
+    g = gen(T)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).reshape(-1)
+    order = torch.argsort(ids, stable=True)
+    off = np.concatenate([[0], np.cumsum(np.bincount(ids.numpy(), minlength=E))]).astype(np.int32)
+    tok = (order // k).int()
+    row_w = torch.rand(T, k, generator=g).reshape(-1)[order]
+    offd = torch.from_numpy(off).to(DEV)
+    rows = x[tok.numpy()]
+    ref, tol = experts_tolerance(rows, w13, w2, off, fmt, row_w.numpy().astype(np.float64))
+    y = ops.expert_rows_mx(xc, xs, offd, w13c, w13s, w2c, w2s, order.int().to(DEV), fmt,
+                           row_w=row_w.to(DEV), tok_of=tok.to(DEV))
+    got = to_np(y).astype(np.float64)[order.numpy()]
+    assert np.all(np.abs(got - ref) <= tol * (1 + 1e-6)), np.max(np.abs(got - ref) / tol)
+    # the rows already grouped, in their own order: the same bits
+    cs, ss = xc[tok.long().to(DEV)].contiguous(), xs[:, tok.long().to(DEV)].contiguous()
+    y2 = ops.expert_rows_mx(cs, ss, offd, w13c, w13s, w2c, w2s, None, fmt, row_w=row_w.to(DEV))
+    assert torch.equal(y2, y[order.to(DEV)])
+
+
+def test_expert_rows_mx_token_outside_counts_as_zeros():
+    xc, xs, _ = operands(4, 64, "mxfp8", 1)
+    w13c, w13s, _ = operands(64, 64, "mxfp8", 2, lead=2)
+    w2c, w2s, _ = operands(64, 32, "mxfp8", 3, lead=2)
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
+    tok = torch.tensor([0, -1, 4, 3], dtype=torch.int32, device=DEV)
+    y = ops.expert_rows_mx(xc, xs, off, w13c, w13s, w2c, w2s, None, "mxfp8", tok_of=tok)
+    assert (y[1:3] == 0).all() and (y[0] != 0).any() and (y[3] != 0).any()
