@@ -366,9 +366,9 @@ MOE_API int32_t moe_rmsnorm(const void* x, const float* gamma, float eps, int32_
  *   scales  uint8 [ceil(K/128)][rows][4]: the byte of block b of row r at
  *           [b/4][r][b%4]; bytes of blocks past K must be 0
  * A stack of matrices [G, rows, K] has G such arrays of each, one after the
- * other.  K is a multiple of 32 (<= 16384).  codes, bf16 inputs and xn are
- * 16-byte aligned, bf16 outputs of products 32-byte, scales 4-byte
- * (MOE_ERR_INVALID_ARG).  Forward only, like the block itself. */
+ * other.  K is a multiple of 32 (<= 16384).  codes, bf16 inputs, xn and
+ * the scales of weights are 16-byte aligned, bf16 outputs of products 32-byte,
+ * the scales of rows 4-byte (MOE_ERR_INVALID_ARG).  Forward only, like the block itself. */
 typedef enum {
   MOE_MXFP8 = 1, /* E4M3 elements */
   MOE_MXFP4 = 2  /* E2M1 elements */
@@ -384,7 +384,7 @@ MOE_API int32_t moe_mx_quantize(const void* x, int32_t groups, int32_t rows, int
                                 int32_t fmt, uint8_t* codes, uint8_t* scales, void* stream);
 
 /* MX -> bf16: x = bf16(element * 2^p), NaN for a block of scale byte 255.
- * Exact for what moe_mx_quantize gives, except below bf16's smallest value. */
+ * Exact for what moe_mx_quantize gives wherever bf16 holds the value. */
 MOE_API int32_t moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t groups,
                                   int32_t rows, int32_t K, int32_t fmt, void* x, void* stream);
 

@@ -1205,7 +1205,7 @@ int32_t moe_grouped_mm_mx(const uint8_t* x_codes, const uint8_t* x_scales, const
     return MOE_ERR_INVALID_ARG;
   if (!row_dest && y_rows < R) return MOE_ERR_INVALID_ARG;
   if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(y, 32) || !aligned(x_scales, 4) ||
-      !aligned(w_scales, 4))
+      !aligned(w_scales, 16))
     return MOE_ERR_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, moe_grouped_mm_mx_workspace_bytes(R, E, N, K)))
     return MOE_ERR_WORKSPACE;
@@ -1243,8 +1243,8 @@ int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int3
     return MOE_ERR_INVALID_ARG;
   if ((!tok_of && T != R) || (!row_dest && y_rows < R)) return MOE_ERR_INVALID_ARG;
   if (!aligned(x_codes, 16) || !aligned(w13_codes, 16) || !aligned(w2_codes, 16) ||
-      !aligned(y, 32) || !aligned(x_scales, 4) || !aligned(w13_scales, 4) ||
-      !aligned(w2_scales, 4))
+      !aligned(y, 32) || !aligned(x_scales, 4) || !aligned(w13_scales, 16) ||
+      !aligned(w2_scales, 16))
     return MOE_ERR_INVALID_ARG;
   const MxExpertsLayout L = mx_experts_layout(R, H, I, fmt, tok_of != nullptr);
   if (!ws_ok(workspace, workspace_bytes, L.total)) return MOE_ERR_WORKSPACE;

@@ -15,16 +15,28 @@
 // (MXFP8, 4 MMAs of K = 32) or 256 (MXFP4, 4 MMAs of K = 64).  Bytes a step and
 // MMA time a step are those of the bf16 kernel (grouped_gemm.cu), for two and
 // four times the elements.  Each CTA loads its 128 rows of A and half of the B
-// tile; the scales of both (its own rows' for A, all 256 columns' for B) come
-// by 4-byte cp.async straight into the layout that tcgen05.cp moves to TMEM:
-// 16-byte row l holds the words of tile rows l, l+32, l+64, l+96.
-// Warp roles (both CTAs):
-//   warp 0      TMA loads of A and B (counted on the leader CTA's barrier)
-//   warp 1      TMEM; in the leader one thread copies the scales to TMEM and
-//               issues the MMAs
-//   warps 2..9  epilogue, as in grouped_gemm.cu
-//   warps 10,11 scales of A and of B
-// TMEM: columns 0..255 the accumulator, 256 + 32 s.. the scales of stage s.
+// tile, its own rows' scales of A and all 256 columns' scales of B.
+// tcgen05.cp wants the scale words of 128 operand rows as 32 rows of 16 bytes,
+// row l holding those of operand rows l, l+32, l+64, l+96.  B's rows are laid
+// in shared memory so that this is the order of its words in memory: operand
+// row j*32 + l is matrix row 4l + j (four TMA boxes of every fourth row), one
+// TMA copy then brings 128 words as they are, and the epilogue reads
+// accumulator column j*32 + l as output column 4l + j.  A's tiles start at any
+// row, which TMA does not take for 4-byte words: four warps (one per lane
+// quarter) load them into registers and store them to TMEM, 16 words a row
+// (2048 elements) at a time, ahead of the MMAs.  Bringing them through shared
+// memory a K step at a time needed a proxy fence and a release across the pair
+// in every step: 1.3 us a step instead of 0.3.
+// Warp roles (both CTAs; registers move from the first and last warpgroup to
+// the epilogue, whose threads hold 128 accumulator columns):
+//   warp 0       TMA loads of A, B and B's scales (counted on the leader CTA's
+//                barrier)
+//   warp 1       TMEM; in the leader one thread copies B's scales to TMEM and
+//                issues the MMAs
+//   warps 4..11  epilogue, as in grouped_gemm.cu
+//   warps 12..15 scales of A
+// TMEM: columns 0..255 the accumulator, 256.. two buffers of 64 for A's scales,
+// 384.. 16 per stage for B's.
 // The accumulator is not double-buffered (two of them leave no columns for the
 // scales); the epilogue reads it whole into registers and hands it back before
 // it computes or stores anything.
@@ -49,27 +61,31 @@ constexpr int STAGES = 6;
 constexpr int A_BYTES = BM * KB;
 constexpr int B_BYTES = BN / 2 * KB;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int B_BOX = 32;        // B rows per TMA box (every fourth row of the matrix)
 constexpr int SF_BYTES = 512;    // scale words of 128 rows
-constexpr int THREADS = 384;
+constexpr int THREADS = 512;
+constexpr int EPI_WARP0 = 4;
+constexpr int SFA_WARP0 = 12;
 constexpr int EPI_WARPS = 8;
-constexpr int SF_LAG = 2;        // K steps of scales in flight per warp
+constexpr int SFA_WORDS = 16;    // words per row in a buffer of A's scales
 constexpr int MAX_GROUPS = 128;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t TMEM_SF = 256;        // first scale column
-constexpr uint32_t TMEM_SF_STAGE = 32;   // columns per stage: A's words at +0, B's at +8
-constexpr uint32_t TMEM_SFB = 8;
+constexpr uint32_t TMEM_SFA = 256;       // + 64 per buffer, 4 per word
+constexpr uint32_t TMEM_SFB = 384;       // + 16 per stage, 8 per word, 4 per half
 constexpr unsigned FULL = 0xffffffffu;
 
 template <int FMT>
 struct Fmt {
   static constexpr int kWords = FMT == MOE_MXFP8 ? 1 : 2;  // scale words per row and K step
-  static constexpr int kSf = kWords * 3 * SF_BYTES;        // A, then both halves of B
+  static constexpr int kSf = kWords * 2 * SF_BYTES;        // B's, both halves
   static constexpr size_t kSmem = 1024 + (size_t)STAGES * (STAGE_BYTES + kSf);
 };
 
 struct __align__(8) SmemTail {
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
+  uint64_t sfa_full[2];
+  uint64_t sfa_empty[2];
   uint64_t tfull;
   uint64_t tempty;
   uint64_t drain;
@@ -162,23 +178,64 @@ __device__ __forceinline__ uint64_t sdesc_rows16(uint32_t saddr) {
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const uint32_t* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// 32 columns of this warp's lane quarter.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
 }
 
-// Arrive on a barrier of another CTA of the cluster, releasing this thread's
-// shared-memory writes to it.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+// Moves registers between warpgroups: 4 warpgroups are launched with 128 each.
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+constexpr int REGS_ISSUE = 64, REGS_EPI = 184, REGS_SFA = 80;
+static_assert(REGS_ISSUE + 2 * REGS_EPI + REGS_SFA <= 4 * 128, "registers of the launch");
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
 }
 
-__device__ __forceinline__ void fence_acquire_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+// Tile loads to a shared-memory address, completion counted on the barrier at
+// cluster address mbar (the leader's).
+__device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap* map, uint32_t mbar,
+                                               int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* map, uint32_t mbar,
+                                               int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
 }
 
 template <int FMT, int EPI>
@@ -196,9 +253,12 @@ __device__ __forceinline__ void epilogue(const MxGemmArgs& a, const uint32_t (&v
       if (col0 + c < a.n_valid) {
         uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          pk[i] = pack_bf16x2(w * __uint_as_float(v[c + 2 * i]),
-                              w * __uint_as_float(v[c + 2 * i + 1]));
+        for (int i = 0; i < 16; ++i) {
+          // output columns n, n + 1 of this half: accumulator columns n%4*32 + n/4, ...
+          const int n = c + 2 * i;
+          pk[i] = pack_bf16x2(w * __uint_as_float(v[(n & 3) * 32 + (n >> 2)]),
+                              w * __uint_as_float(v[((n + 1) & 3) * 32 + (n >> 2)]));
+        }
         __nv_bfloat16* dst =
             static_cast<__nv_bfloat16*>(a.out) + (size_t)dest * a.n_valid + col0 + c;
         st_global_v8(dst, pk);
@@ -206,7 +266,8 @@ __device__ __forceinline__ void epilogue(const MxGemmArgs& a, const uint32_t (&v
       }
     }
   } else {
-    // gate in v[0..63], up in v[64..127]: two blocks of h, half a word of scales
+    // gate in v[0..63], up in v[64..127], column 4l + j at j*16 + l: two blocks of
+    // h, half a word of scales
     const int col0 = t.nt * (BN / 2) + half * 64;
     uint32_t bytes = 0;
 #pragma unroll
@@ -216,7 +277,8 @@ __device__ __forceinline__ void epilogue(const MxGemmArgs& a, const uint32_t (&v
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          h[i] = silu_f(__uint_as_float(v[32 * b + i])) * __uint_as_float(v[64 + 32 * b + i]);
+          const int n = 32 * b + i, c = (n & 3) * 16 + (n >> 2);
+          h[i] = silu_f(__uint_as_float(v[c])) * __uint_as_float(v[64 + c]);
           m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
         }
         const uint32_t byte = mx_scale_byte<FMT>(m);
@@ -240,7 +302,8 @@ __device__ __forceinline__ void epilogue(const MxGemmArgs& a, const uint32_t (&v
 template <int FMT, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     grouped_mx_kernel(const __grid_constant__ CUtensorMap tmA,
-                      const __grid_constant__ CUtensorMap tmB, const MxGemmArgs args) {
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmSB, const MxGemmArgs args) {
   using F = Fmt<FMT>;
   pdl_launch_dependents();
   pdl_wait();
@@ -271,8 +334,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&st.full[s], 1 + 4);  // leader: its producer, the scale warps of both CTAs
-      mbar_init(&st.empty[s], 1);     // both: one commit from the leader's MMA thread
+      mbar_init(&st.full[s], 1);   // leader: its producer's expect-tx arrive
+      mbar_init(&st.empty[s], 1);  // both: one commit from the leader's MMA thread
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&st.sfa_full[b], 8);   // leader: the scale warps of both CTAs
+      mbar_init(&st.sfa_empty[b], 1);  // both: one commit
     }
     mbar_init(&st.tfull, 1);
     mbar_init(&st.tempty, 2 * EPI_WARPS);  // leader: every epilogue warp of both CTAs
@@ -283,6 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSB);
   }
   __syncthreads();
   if (threadIdx.x == 0 && blockIdx.x == 0 && st.bad_offsets)
@@ -330,31 +398,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const WaitCtx wc{&st.abort_flag, args.status, args.timeout_ns};
   const int k_steps = (args.k_bytes + KB - 1) / KB;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------ TMA producer (both CTAs)
+  if (warp < EPI_WARP0) {
+    regs_dec<REGS_ISSUE>();
+    // The issuing warps run their loops with all lanes and elect one to issue, so
+    // that stages, addresses and descriptors stay in uniform registers: with one
+    // lane in the loop a K step took 960 cycles to issue, twice its MMAs' time.
+    const uint32_t smem0 = smem_u32(smem), sf0 = smem_u32(smem_sf);
+    if (warp == 0 || warp == 2) {
+      // ------------------------------------------------ TMA producers (both CTAs):
+      // A and B's scales, and the barrier's byte count (warp 0); B (warp 2)
       int stage = 0;
       uint32_t phase = 0;
       uint32_t armed = 0, armed_parity = 0;
       bool ok = true;
+      const uint32_t full0 = mapa_shared(smem_u32(&st.full[0]), 0);  // the leader's barriers
       for (int tile = cluster; ok && tile < total; tile += nclusters) {
         const Tile t = tile_at(tile, args.n_tiles, args.groups, st.mt_start, st.row_start);
         const int a_row = t.row0 + BM * (int)rank;
-        const int b_row = t.nt * args.n_out_tile + (int)rank * args.b_second;
+        const int b_row = (t.nt * args.n_out_tile + (int)rank * args.b_second) >> 2;
         const bool load_a = t.rows > BM * (int)rank;  // a half without rows loads none
-        const uint32_t tx = 2 * B_BYTES + A_BYTES + (t.rows > BM ? A_BYTES : 0);
+        const int n0 = t.nt * args.n_out_tile, n1 = n0 + args.b_second;
+        int sf_row = t.g * args.words;
+        const uint32_t tx = 2 * (B_BYTES + 2 * F::kWords * SF_BYTES) + A_BYTES +
+                            (t.rows > BM ? A_BYTES : 0);
+        int kb = 0;
         for (int ks = 0; ks < k_steps; ++ks) {
-          if (!mbar_wait(&st.empty[stage], phase ^ 1u, wc, 61)) {
+          if (!__all_sync(FULL, mbar_wait(&st.empty[stage], phase ^ 1u, wc, 61))) {
             ok = false;
             break;
           }
-          uint8_t* sa = smem + (size_t)stage * STAGE_BYTES;
-          const uint32_t full_leader = mapa_shared(smem_u32(&st.full[stage]), 0);
-          if (leader) mbar_arrive_expect_tx(&st.full[stage], tx);
-          if (load_a) tma_load_2d_pair(sa, &tmA, full_leader, ks * KB, a_row);
-          tma_load_3d_pair(sa + A_BYTES, &tmB, full_leader, ks * KB, b_row, t.g);
+          const uint32_t full = full0 + 8 * stage;
+          const uint32_t sa = smem0 + stage * STAGE_BYTES;
+          if (elect_one()) {
+            if (warp == 0) {
+              if (leader) mbar_arrive_expect_tx(&st.full[stage], tx);
+              if (load_a) tma_load_2d_at(sa, &tmA, full, kb, a_row);
+              const uint32_t sb = sf0 + stage * F::kSf;
+              tma_load_2d_at(sb, &tmSB, full, n0, sf_row);
+              tma_load_2d_at(sb + F::kWords * SF_BYTES, &tmSB, full, n1, sf_row);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tma_load_4d_at(sa + A_BYTES + j * B_BOX * KB, &tmB, full, kb, j, b_row, t.g);
+            }
+          }
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          kb += KB;
+          sf_row += F::kWords;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -366,64 +457,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if ((armed >> s) & 1u)
             mbar_wait_drain(&st.full[s], (armed_parity >> s) & 1u, args.timeout_ns);
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ------------------------------------------------ scales to TMEM and pair MMAs (leader)
-      int stage = 0;
-      uint32_t phase = 0, acc_phase = 0;
+    } else if (warp == 1 && leader) {
+      // ------------------------------------------------ B's scales to TMEM and pair MMAs (leader)
+      constexpr int SFA_STEPS = SFA_WORDS / F::kWords;  // K steps per buffer of A's scales
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0, sfa_phase = 0;
       bool ok = true;
+      const uint64_t da0 = sdesc_kmajor_sw128(smem0), dsf0 = sdesc_rows16(sf0);
+      const int last = args.k_bytes - (k_steps - 1) * KB;  // bytes of a row in the last step
       for (int tile = cluster; ok && tile < total; tile += nclusters) {
-        if (!mbar_wait(&st.tempty, acc_phase ^ 1u, wc, 62)) break;
-        tc_fence_after_sync();
+        if (!__all_sync(FULL, mbar_wait(&st.tempty, acc_phase ^ 1u, wc, 62))) break;
+        int chunk_left = 0;
+        uint32_t sfa = 0;
         for (int ks = 0; ks < k_steps; ++ks) {
-          if (!mbar_wait(&st.full[stage], phase, wc, 63)) {
+          if (chunk_left == 0) {
+            if (!__all_sync(FULL, mbar_wait(&st.sfa_full[buf], sfa_phase, wc, 66))) {
+              ok = false;
+              break;
+            }
+            chunk_left = SFA_STEPS;
+            sfa = tmem_base + TMEM_SFA + 64 * buf;
+          }
+          if (!__all_sync(FULL, mbar_wait(&st.full[stage], phase, wc, 63))) {
             ok = false;
             break;
           }
-          fence_acquire_cluster();  // the peer's scale words
           tc_fence_after_sync();
-          const uint32_t sa = smem_u32(smem + (size_t)stage * STAGE_BYTES);
-          const uint32_t sf = smem_u32(smem_sf + (size_t)stage * F::kSf);
-          const uint32_t sfa = tmem_base + TMEM_SF + stage * TMEM_SF_STAGE;
-          const uint32_t sfb = sfa + TMEM_SFB;
+          --chunk_left;
+          const bool chunk_done = chunk_left == 0 || ks + 1 == k_steps;
+          const uint32_t sfb = tmem_base + TMEM_SFB + 16 * stage;
+          const uint64_t dsf = dsf0 + static_cast<uint64_t>(stage * (F::kSf >> 4));
+          const uint64_t da = da0 + static_cast<uint64_t>(stage * (STAGE_BYTES >> 4));
+          const uint64_t db = da + (A_BYTES >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int w = 0; w < F::kWords; ++w) {
-            tmem_copy_sf_pair(sfa + 4 * w, sdesc_rows16(sf + w * SF_BYTES));
+            for (int w = 0; w < F::kWords; ++w)
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb)
-              tmem_copy_sf_pair(sfb + 8 * w + 4 * hb,
-                                sdesc_rows16(sf + (F::kWords + 2 * w + hb) * SF_BYTES));
+              for (int hb = 0; hb < 2; ++hb)
+                tmem_copy_sf_pair(sfb + 8 * w + 4 * hb,
+                                  dsf + (F::kWords * hb + w) * (SF_BYTES >> 4));
+            // 32 bytes of every row per MMA; the scale word, and the byte in it
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (ks + 1 < k_steps || kk * 32 < last)
+                umma_mx_pair<FMT>(
+                    tmem_base, da + 2 * kk, db + 2 * kk,
+                    idesc_sf(idesc_mx<FMT>(), FMT == MOE_MXFP8 ? kk : 2 * (kk & 1)),
+                    sfa + 4 * (kk * F::kWords / 4), sfb + 8 * (kk * F::kWords / 4),
+                    (ks | kk) != 0 ? 1u : 0u);
+            umma_commit_pair_mask(&st.empty[stage], 0x3);
+            if (chunk_done) umma_commit_pair_mask(&st.sfa_empty[buf], 0x3);
+            if (ks + 1 == k_steps) umma_commit_pair_mask(&st.tfull, 0x3);
           }
-          const uint64_t da = sdesc_kmajor_sw128(sa);
-          const uint64_t db = sdesc_kmajor_sw128(sa + A_BYTES);
-          const int left = args.k_bytes - ks * KB;  // 32 bytes of every row per MMA
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk * 32 < left) {
-              const int w = kk * F::kWords / 4;  // the scale word, and the byte in it
-              const uint32_t id = FMT == MOE_MXFP8 ? kk : 2 * (kk & 1);
-              umma_mx_pair<FMT>(tmem_base, da + 2 * kk, db + 2 * kk, idesc_sf(idesc_mx<FMT>(), id),
-                                sfa + 4 * w, sfb + 8 * w, (ks | kk) != 0 ? 1u : 0u);
-            }
+          sfa += 4 * F::kWords;
+          if (chunk_done) {
+            chunk_left = 0;
+            buf ^= 1;
+            if (buf == 0) sfa_phase ^= 1u;
           }
-          umma_commit_pair_mask(&st.empty[stage], 0x3);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        umma_commit_pair_mask(&st.tfull, 0x3);
         acc_phase ^= 1u;
       }
-      umma_commit_pair_mask(&st.drain, 0x1);  // all of this thread's MMAs are done
-      mbar_wait_drain(&st.drain, 0, args.timeout_ns);
+      if (elect_one()) {
+        umma_commit_pair_mask(&st.drain, 0x1);  // all of this warp's MMAs are done
+        mbar_wait_drain(&st.drain, 0, args.timeout_ns);
+      }
+      __syncwarp();
     }
-  } else if (warp < 10) {
-    // ------------------------------------------------ epilogue warps 2..9 (both CTAs)
+  } else if (warp < SFA_WARP0) {
+    regs_inc<REGS_EPI>();
+    // ------------------------------------------------ epilogue warps 4..11 (both CTAs)
     const int q = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - EPI_WARP0) >> 2;
     const int r_in_tile = q * 32 + lane;
     const uint32_t tempty_leader = mapa_shared(smem_u32(&st.tempty), 0);
     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
@@ -437,13 +546,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tc_fence_after_sync();
       uint32_t v[128];
       if constexpr (EPI == MX_SWIGLU) {
-        // accumulator columns [0,128) gate, [128,256) up; this half: 64 of each
+        // accumulator columns [0,128) gate, [128,256) up; this half: output columns
+        // half*64 + [0,64), which are 16 consecutive columns of each j
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tmem_ld_32x32b_x32(tb + half * 64 + 32 * c,
-                             *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
-          tmem_ld_32x32b_x32(tb + BN / 2 + half * 64 + 32 * c,
-                             *reinterpret_cast<uint32_t(*)[32]>(v + 64 + 32 * c));
+        for (int j = 0; j < 4; ++j) {
+          tmem_ld_32x32b_x16(tb + 32 * j + half * 16,
+                             *reinterpret_cast<uint32_t(*)[16]>(v + 16 * j));
+          tmem_ld_32x32b_x16(tb + BN / 2 + 32 * j + half * 16,
+                             *reinterpret_cast<uint32_t(*)[16]>(v + 64 + 16 * j));
         }
       } else {
 #pragma unroll
@@ -459,68 +569,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       acc_phase ^= 1u;
     }
   } else {
-    // ------------------------------------------------ scale warps: A's rows, B's columns
-    const bool is_a = warp == 10;
-    const int words = args.words;
-    int stage = 0, done = 0, issued = 0;
+    regs_dec<REGS_SFA>();
+    // ------------------------------------------------ scales of this CTA's rows of A
+    const uint32_t full_leader[2] = {mapa_shared(smem_u32(&st.sfa_full[0]), 0),
+                                     mapa_shared(smem_u32(&st.sfa_full[1]), 0)};
+    const uint32_t tq = tmem_base + TMEM_SFA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    int buf = 0;
     uint32_t phase = 0;
     bool ok = true;
-    auto arrive_oldest = [&]() {
-      fence_proxy_async_smem();  // cp.async writes -> tcgen05.cp reads
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&st.full[done % STAGES]), 0));
-      ++done;
-    };
     for (int tile = cluster; ok && tile < total; tile += nclusters) {
       const Tile t = tile_at(tile, args.n_tiles, args.groups, st.mt_start, st.row_start);
-      const int a_row0 = t.row0 + BM * (int)rank;
-      const int a_rows = min(BM, t.rows - BM * (int)rank);  // may be <= 0
-      for (int ks = 0; ks < k_steps; ++ks) {
-        const bool got = mbar_wait(&st.empty[stage], phase ^ 1u, wc, 65);
+      const int rows = min(BM, t.rows - BM * (int)rank);  // may be <= 0
+      const uint32_t* src = args.a_scales + t.row0 + BM * (int)rank + lane;
+      for (int w0 = 0; w0 < args.words; w0 += SFA_WORDS) {
+        const bool got = mbar_wait(&st.sfa_empty[buf], phase ^ 1u, wc, 65);
         if (!__all_sync(FULL, got)) {
           ok = false;
           break;
         }
-        const uint32_t sf = smem_u32(smem_sf + (size_t)stage * F::kSf) + lane * 16;
+        tc_fence_after_sync();
+        const int nw = min(SFA_WORDS, args.words - w0);
+#pragma unroll 1
+        for (int h = 0; h < nw; h += 8) {  // 8 words of rows lane + 32 j: column 4 w + j
+          uint32_t v[32];
 #pragma unroll
-        for (int w = 0; w < F::kWords; ++w) {
-          const int kw = ks * F::kWords + w;
-          if (kw < words) {
-            if (is_a) {
-              const uint32_t* src = args.a_scales + (size_t)kw * args.rows + a_row0;
+          for (int w = 0; w < 8; ++w)
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (lane + 32 * j < a_rows)
-                  cp_async_4(sf + w * SF_BYTES + 4 * j, src + lane + 32 * j);
-            } else {
-              const uint32_t* src =
-                  args.b_scales + ((size_t)t.g * words + kw) * args.n_rows;
-#pragma unroll
-              for (int hb = 0; hb < 2; ++hb) {
-                const int n0 = t.nt * args.n_out_tile + hb * args.b_second;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (n0 + lane + 32 * j < args.n_rows)
-                    cp_async_4(sf + (F::kWords + 2 * w + hb) * SF_BYTES + 4 * j,
-                               src + n0 + lane + 32 * j);
-              }
-            }
-          }
+            for (int j = 0; j < 4; ++j)
+              v[4 * w + j] = h + w < nw && lane + 32 * j < rows
+                                 ? src[(size_t)(w0 + h + w) * args.rows + 32 * j]
+                                 : 0u;
+          tmem_st_32x32b_x32(tq + 64 * buf + 4 * h, v);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        ++issued;
-        if (issued > SF_LAG) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(SF_LAG) : "memory");
-          arrive_oldest();
-        }
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(full_leader[buf]);
+        buf ^= 1;
+        if (buf == 0) phase ^= 1u;
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    while (done < issued) arrive_oldest();
   }
 
   // both CTAs are done with the accumulator and the scales before either frees TMEM or exits
@@ -547,26 +635,50 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Rows of bytes in boxes of 128 bytes x 128 rows, 128-byte swizzle; bytes past
-// a row's end and rows past a matrix's end read 0.
-cudaError_t make_tmap_bytes(CUtensorMap* map, const void* base, uint64_t groups, uint64_t rows,
-                            uint64_t row_bytes) {
+cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
+                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                   CUtensorMapSwizzle swizzle) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {row_bytes, rows, groups};
-  const cuuint64_t strides[2] = {row_bytes, rows * row_bytes};
-  const cuuint32_t box[3] = {KB, BM, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r =
-      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups ? 3 : 2, const_cast<void*>(base), dims,
-         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      fn(map, type, rank, const_cast<void*>(base), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Rows of codes in boxes of 128 bytes x 128 rows; bytes past a row's end and
+// rows past the last one read 0.
+cudaError_t make_tmap_a(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes) {
+  const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {KB, BM};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+                CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The matrices' rows 4q + j in boxes of 128 bytes x one j x 32 q.
+cudaError_t make_tmap_b(CUtensorMap* map, const void* base, uint64_t groups, uint64_t rows,
+                        uint64_t row_bytes) {
+  const cuuint64_t dims[4] = {row_bytes, 4, rows / 4, groups};
+  const cuuint64_t strides[3] = {row_bytes, 4 * row_bytes, rows * row_bytes};
+  const cuuint32_t box[4] = {KB, 1, B_BOX, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box,
+                CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The matrices' scale words, 128 columns of one K step a box.
+cudaError_t make_tmap_sb(CUtensorMap* map, const void* base, uint64_t word_rows, uint64_t rows,
+                         uint32_t step_words) {
+  const cuuint64_t dims[2] = {rows, word_rows}, strides[1] = {rows * 4};
+  const cuuint32_t box[2] = {BM, step_words};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, base, dims, strides, box,
+                CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 template <int FMT, int EPI>
-cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const MxGemmArgs& args,
-                   int grid, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSB,
+                   const MxGemmArgs& args, int grid, cudaStream_t stream) {
   constexpr size_t smem = Fmt<FMT>::kSmem + sizeof(SmemTail);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<int> smem_set[MAX_DEVICES];
@@ -574,7 +686,7 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const MxGemmA
       set_smem_limit_per_device(grouped_mx_kernel<FMT, EPI>, (int)smem, smem_set);
   if (e != cudaSuccess) return e;
   return launch_chained(grouped_mx_kernel<FMT, EPI>, dim3(grid), dim3(THREADS), smem, stream, tmA,
-                        tmB, args);
+                        tmB, tmSB, args);
 }
 
 // Rows of narrow tokens in expert order: codes[r] = tokens[tok_of[r]] (16-byte
@@ -606,10 +718,12 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_grouped_mx(int fmt, int epi, const void* a, const void* b, MxGemmArgs args,
                               cudaStream_t stream) {
   if (args.groups > MAX_GROUPS) return cudaErrorInvalidValue;
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmSB;
   cudaError_t e;
-  if ((e = make_tmap_bytes(&tmA, a, 0, args.rows, args.k_bytes)) != cudaSuccess) return e;
-  if ((e = make_tmap_bytes(&tmB, b, args.groups, args.n_rows, args.k_bytes)) != cudaSuccess)
+  if ((e = make_tmap_a(&tmA, a, args.rows, args.k_bytes)) != cudaSuccess) return e;
+  if ((e = make_tmap_b(&tmB, b, args.groups, args.n_rows, args.k_bytes)) != cudaSuccess) return e;
+  if ((e = make_tmap_sb(&tmSB, args.b_scales, (uint64_t)args.groups * args.words, args.n_rows,
+                        fmt == MOE_MXFP8 ? 1 : 2)) != cudaSuccess)
     return e;
   args.n_out_tile = epi == MX_SWIGLU ? BN / 2 : BN;
   args.n_tiles = (args.n_valid + args.n_out_tile - 1) / args.n_out_tile;
@@ -618,10 +732,10 @@ cudaError_t launch_grouped_mx(int fmt, int epi, const void* a, const void* b, Mx
   const int sms = num_sms() & ~1;
   const int grid = (int)(2 * tiles < sms ? 2 * tiles : sms);
   if (fmt == MOE_MXFP8)
-    return epi == MX_SWIGLU ? launch<MOE_MXFP8, MX_SWIGLU>(tmA, tmB, args, grid, stream)
-                            : launch<MOE_MXFP8, MX_ROWS>(tmA, tmB, args, grid, stream);
-  return epi == MX_SWIGLU ? launch<MOE_MXFP4, MX_SWIGLU>(tmA, tmB, args, grid, stream)
-                          : launch<MOE_MXFP4, MX_ROWS>(tmA, tmB, args, grid, stream);
+    return epi == MX_SWIGLU ? launch<MOE_MXFP8, MX_SWIGLU>(tmA, tmB, tmSB, args, grid, stream)
+                            : launch<MOE_MXFP8, MX_ROWS>(tmA, tmB, tmSB, args, grid, stream);
+  return epi == MX_SWIGLU ? launch<MOE_MXFP4, MX_SWIGLU>(tmA, tmB, tmSB, args, grid, stream)
+                          : launch<MOE_MXFP4, MX_ROWS>(tmA, tmB, tmSB, args, grid, stream);
 }
 
 cudaError_t launch_gather_mx(const uint8_t* codes, const uint8_t* scales, const int* tok_of, int T,
