@@ -22,21 +22,21 @@
 // row j*32 + l is matrix row 4l + j (four TMA boxes of every fourth row), one
 // TMA copy then brings 128 words as they are, and the epilogue reads
 // accumulator column j*32 + l as output column 4l + j.  A's tiles start at any
-// row, which TMA does not take for 4-byte words: four warps (one per lane
-// quarter) load them into registers and store them to TMEM, 16 words a row
-// (2048 elements) at a time, ahead of the MMAs.  Bringing them through shared
-// memory a K step at a time needed a proxy fence and a release across the pair
-// in every step: 1.3 us a step instead of 0.3.
-// Warp roles (both CTAs; registers move from the first and last warpgroup to
-// the epilogue, whose threads hold 128 accumulator columns):
-//   warp 0       TMA loads of A, B and B's scales (counted on the leader CTA's
+// row, which TMA does not take for 4-byte words: a warp loads them and writes
+// them to shared memory in that order, 16 words a row (2048 elements) at a
+// time, because the proxy fence and the release across the pair that this
+// takes cost 1 us when they are paid in every K step.
+// Warp roles (both CTAs):
+//   warp 0       TMA loads of A and of B's scales (counted on the leader CTA's
 //                barrier)
-//   warp 1       TMEM; in the leader one thread copies B's scales to TMEM and
-//                issues the MMAs
-//   warps 4..11  epilogue, as in grouped_gemm.cu
-//   warps 12..15 scales of A
-// TMEM: columns 0..255 the accumulator, 256.. two buffers of 64 for A's scales,
-// 384.. 16 per stage for B's.
+//   warp 1       TMEM; in the leader it copies the scales to TMEM and issues the
+//                MMAs
+//   warp 2       TMA loads of B
+//   warp 3       scales of A
+//   warps 4..19  epilogue: four warps per TMEM lane quarter, 64 accumulator
+//                columns a thread (eight warps of 128 columns were bound by their
+//                own latency, and left no registers for the rest)
+// TMEM: columns 0..255 the accumulator, 256 + 32 s.. the scales of stage s.
 // The accumulator is not double-buffered (two of them leave no columns for the
 // scales); the epilogue reads it whole into registers and hands it back before
 // it computes or stores anything.
@@ -57,33 +57,39 @@ constexpr int BM = 128;          // rows per CTA
 constexpr int TILE_M = 2 * BM;   // rows per pair tile
 constexpr int BN = 256;          // accumulator columns
 constexpr int KB = 128;          // bytes of a row per K step
-constexpr int STAGES = 6;
+constexpr int MAX_STAGES = 6;
 constexpr int A_BYTES = BM * KB;
 constexpr int B_BYTES = BN / 2 * KB;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int B_BOX = 32;        // B rows per TMA box (every fourth row of the matrix)
 constexpr int SF_BYTES = 512;    // scale words of 128 rows
-constexpr int THREADS = 512;
+constexpr int THREADS = 640;
 constexpr int EPI_WARP0 = 4;
-constexpr int SFA_WARP0 = 12;
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16;
+constexpr int EPI_COLS = 64;     // accumulator columns of an epilogue thread
+constexpr int OUT_PITCH = BN * 2 + 16;  // bytes of an output row in shared memory (no conflicts)
 constexpr int SFA_WORDS = 16;    // words per row in a buffer of A's scales
+constexpr int SFA_BYTES = SFA_WORDS * SF_BYTES;
 constexpr int MAX_GROUPS = 128;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t TMEM_SFA = 256;       // + 64 per buffer, 4 per word
-constexpr uint32_t TMEM_SFB = 384;       // + 16 per stage, 8 per word, 4 per half
+constexpr uint32_t TMEM_SF = 256;        // + 32 per stage: A, 4 per word, ...
+constexpr uint32_t TMEM_SFB = 8;         // ... B, 8 per word, 4 per half
 constexpr unsigned FULL = 0xffffffffu;
 
-template <int FMT>
-struct Fmt {
+template <int FMT, int EPI>
+struct Shape {
   static constexpr int kWords = FMT == MOE_MXFP8 ? 1 : 2;  // scale words per row and K step
-  static constexpr int kSf = kWords * 2 * SF_BYTES;        // B's, both halves
-  static constexpr size_t kSmem = 1024 + (size_t)STAGES * (STAGE_BYTES + kSf);
+  static constexpr int kStages = EPI == MX_ROWS ? 4 : 6;   // rows: room for the output tile
+  static constexpr int kSfb = kWords * 2 * SF_BYTES;       // B's scales, both halves
+  static constexpr int kOffSfb = kStages * STAGE_BYTES;
+  static constexpr int kOffSfa = kOffSfb + kStages * kSfb;
+  static constexpr int kOffOut = kOffSfa + 2 * SFA_BYTES;
+  static constexpr int kOffTail = kOffOut + (EPI == MX_ROWS ? BM * OUT_PITCH : 0);
 };
 
 struct __align__(8) SmemTail {
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
   uint64_t sfa_full[2];
   uint64_t sfa_empty[2];
   uint64_t tfull;
@@ -105,28 +111,53 @@ __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity,
   }
 }
 
+// A value that is the same in all lanes, told to the compiler, which then keeps
+// it (and branches on it) in uniform registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(FULL, v, 0); }
+
 struct Tile {
   int g, row0, rows, nt;
 };
 
-__device__ __forceinline__ Tile tile_at(int tile, int n_tiles, int groups, const int* mts,
-                                        const int* rs) {
-  Tile t;
-  const int mt = tile / n_tiles;
-  t.nt = tile - mt * n_tiles;
-  int lo = 0, hi = groups;  // largest g with mts[g] <= mt (skips empty groups)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (mts[mid] <= mt)
-      lo = mid;
-    else
-      hi = mid;
+// The tiles of one cluster in order: every nclusters-th, columns fastest.  The
+// warp finds the next one's group together (32 groups a look), since a search
+// by one thread, seven dependent loads, cost each role 1,300 cycles a tile.
+struct TileWalk {
+  int g, mt, nt;
+
+  __device__ __forceinline__ void start(int tile, int n_tiles, int groups, const int* mts) {
+    mt = tile / n_tiles;
+    nt = tile - mt * n_tiles;
+    g = 0;
+    seek(groups, mts);
   }
-  t.g = lo;
-  t.row0 = rs[lo] + (mt - mts[lo]) * TILE_M;
-  t.rows = min(TILE_M, rs[lo + 1] - t.row0);
-  return t;
-}
+  __device__ __forceinline__ void next(int dm, int dn, int n_tiles, int groups, const int* mts) {
+    mt += dm;
+    nt += dn;
+    if (nt >= n_tiles) {
+      nt -= n_tiles;
+      ++mt;
+    }
+    seek(groups, mts);
+  }
+  // largest g with mts[g] <= mt (skips empty groups); g is never past it
+  __device__ __forceinline__ void seek(int groups, const int* mts) {
+    unsigned b;
+    do {
+      const int i = min(g + (int)(threadIdx.x & 31), groups);
+      b = __ballot_sync(FULL, mts[i] <= mt && i < groups);
+      g += __popc(b) - 1;
+    } while (b == FULL);
+  }
+  __device__ __forceinline__ Tile tile(const int* mts, const int* rs) const {
+    Tile t;
+    t.g = g;
+    t.nt = nt;
+    t.row0 = uniform(rs[g] + (mt - mts[g]) * TILE_M);
+    t.rows = min(TILE_M, uniform(rs[g + 1]) - t.row0);
+    return t;
+  }
+};
 
 // The same expression as in the bf16 kernels.
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
@@ -178,36 +209,12 @@ __device__ __forceinline__ uint64_t sdesc_rows16(uint32_t saddr) {
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
-// 32 columns of this warp's lane quarter.
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// Moves registers between warpgroups: 4 warpgroups are launched with 128 each.
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-constexpr int REGS_ISSUE = 64, REGS_EPI = 184, REGS_SFA = 80;
-static_assert(REGS_ISSUE + 2 * REGS_EPI + REGS_SFA <= 4 * 128, "registers of the launch");
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -238,64 +245,132 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
+// Arrive on a barrier of the cluster, releasing this thread's shared-memory
+// writes (and those of the warp's lanes before a __syncwarp) to its CTAs.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
+// Acquires at cluster scope a phase that mbar_wait has seen complete.
+__device__ __forceinline__ void mbar_acquire_cluster(uint64_t* bar, uint32_t parity) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(parity)
+      : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// 32 TMEM lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+
+// Accumulator columns of epilogue part 0..3: 64 output columns part*64.. (MX_ROWS),
+// or gate and up of output columns part*32.. (MX_SWIGLU).  Output column 4l + j
+// of a 128-column half lies at j*32 + l.
+template <int EPI>
+__device__ __forceinline__ void load_part(uint32_t tb, int part, uint32_t (&v)[EPI_COLS]) {
+  if constexpr (EPI == MX_ROWS) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      tmem_ld_32x32b_x16(tb + (part >> 1) * 128 + 32 * j + (part & 1) * 16,
+                         *reinterpret_cast<uint32_t(*)[16]>(v + 16 * j));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      tmem_ld_32x32b_x8(tb + 32 * j + part * 8, *reinterpret_cast<uint32_t(*)[8]>(v + 8 * j));
+      tmem_ld_32x32b_x8(tb + BN / 2 + 32 * j + part * 8,
+                        *reinterpret_cast<uint32_t(*)[8]>(v + 32 + 8 * j));
+    }
+  }
+  tmem_ld_wait();
+}
+
+// Named barrier of the four epilogue warps that share a TMEM lane quarter.
+__device__ __forceinline__ void quarter_sync(int q) {
+  asm volatile("bar.sync %0, 128;" ::"r"(q + 1) : "memory");
+}
+
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+}
+
+// t: this CTA's part of the tile; out: the tile's rows in shared memory (MX_ROWS).
 template <int FMT, int EPI>
-__device__ __forceinline__ void epilogue(const MxGemmArgs& a, const uint32_t (&v)[128],
-                                         const Tile& t, int r_in_tile, int half) {
-  if (r_in_tile >= t.rows) return;
+__device__ __forceinline__ void store_part(const MxGemmArgs& a, const uint32_t (&v)[EPI_COLS],
+                                           const Tile& t, int r_in_tile, int part, uint32_t out) {
   const int row = t.row0 + r_in_tile;
   if constexpr (EPI == MX_ROWS) {
-    const int dest = a.row_dest ? a.row_dest[row] : row;
-    if (dest < 0 || dest >= a.out_rows) return;
-    const float w = a.row_w ? a.row_w[row] : 1.0f;
-    const int col0 = t.nt * BN + half * 128;
-#pragma unroll
-    for (int c = 0; c < 128; c += 32) {
-      if (col0 + c < a.n_valid) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          // output columns n, n + 1 of this half: accumulator columns n%4*32 + n/4, ...
-          const int n = c + 2 * i;
-          pk[i] = pack_bf16x2(w * __uint_as_float(v[(n & 3) * 32 + (n >> 2)]),
-                              w * __uint_as_float(v[((n + 1) & 3) * 32 + (n >> 2)]));
-        }
-        __nv_bfloat16* dst =
-            static_cast<__nv_bfloat16*>(a.out) + (size_t)dest * a.n_valid + col0 + c;
-        st_global_v8(dst, pk);
-        st_global_v8(dst + 16, pk + 8);
-      }
+    // The tile goes to shared memory and from there, a row's 256 columns at a
+    // time, by bulk copies.  Stores from registers (64 KB a tile and SM, more
+    // than the SM's path to L2 takes at once) queue up in front of the MMA
+    // warp's barriers: its K steps then took 500 cycles to issue, not 200.
+    const int lane = r_in_tile & 31, q = r_in_tile >> 5;
+    const float w = a.row_w && r_in_tile < t.rows ? a.row_w[row] : 1.0f;
+    // this lane's row of the copies: 8 rows a warp
+    const int crow = q * 32 + part * 8 + lane;
+    int dest = -1;
+    if (lane < 8 && crow < t.rows) {
+      dest = a.row_dest ? a.row_dest[t.row0 + crow] : t.row0 + crow;
+      if (dest >= a.out_rows) dest = -1;
     }
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last tile's copies
+    quarter_sync(q);
+#pragma unroll
+    for (int k = 0; k < EPI_COLS / 8; ++k) {
+      uint32_t pk[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = 8 * k + 2 * i;
+        pk[i] = pack_bf16x2(w * __uint_as_float(v[(n & 3) * 16 + (n >> 2)]),
+                            w * __uint_as_float(v[((n + 1) & 3) * 16 + (n >> 2)]));
+      }
+      st_shared_v4(out + r_in_tile * OUT_PITCH + part * (EPI_COLS * 2) + 16 * k, pk);
+    }
+    fence_proxy_async_smem();  // these writes -> the copies
+    quarter_sync(q);
+    if (dest >= 0)
+      bulk_store(static_cast<__nv_bfloat16*>(a.out) + (size_t)dest * a.n_valid + t.nt * BN,
+                 out + crow * OUT_PITCH, 2 * min(BN, a.n_valid - t.nt * BN));
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   } else {
-    // gate in v[0..63], up in v[64..127], column 4l + j at j*16 + l: two blocks of
-    // h, half a word of scales
-    const int col0 = t.nt * (BN / 2) + half * 64;
-    uint32_t bytes = 0;
+    if (r_in_tile >= t.rows) return;
+    // one block of h: 32 columns of the row
+    const int col0 = t.nt * (BN / 2) + part * MX_BLOCK;
+    uint32_t byte = 0;  // a word's bytes past the last column's block are 0
+    if (col0 < a.n_valid) {
+      float h[MX_BLOCK];
+      uint32_t m = 0;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if (col0 + 32 * b < a.n_valid) {
-        float h[32];
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int n = 32 * b + i, c = (n & 3) * 16 + (n >> 2);
-          h[i] = silu_f(__uint_as_float(v[c])) * __uint_as_float(v[64 + c]);
-          m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
-        }
-        const uint32_t byte = mx_scale_byte<FMT>(m);
-        bytes |= byte << (8 * b);
-        uint32_t q[8];
-        mx_encode<FMT>(h, byte, q);
-        uint8_t* dst = static_cast<uint8_t*>(a.out) +
-                       ((size_t)row * a.n_valid + col0 + 32 * b) / MxFmt<FMT>::kPerByte;
-        if constexpr (FMT == MOE_MXFP8)
-          st_global_v8(dst, q);
-        else
-          *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+      for (int n = 0; n < MX_BLOCK; ++n) {
+        const int c = (n & 3) * 8 + (n >> 2);
+        h[n] = silu_f(__uint_as_float(v[c])) * __uint_as_float(v[32 + c]);
+        m = max(m, __float_as_uint(h[n]) & 0x7fffffffu);
       }
+      byte = mx_scale_byte<FMT>(m);
+      uint32_t q[8];
+      mx_encode<FMT>(h, byte, q);
+      uint8_t* dst =
+          static_cast<uint8_t*>(a.out) + ((size_t)row * a.n_valid + col0) / MxFmt<FMT>::kPerByte;
+      if constexpr (FMT == MOE_MXFP8)
+        st_global_v8(dst, q);
+      else
+        *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
     }
-    // the word's bytes past the last column's block are 0
-    uint16_t* s = reinterpret_cast<uint16_t*>(a.out_scales + (size_t)t.nt * a.rows + row);
-    s[half] = static_cast<uint16_t>(bytes);
+    reinterpret_cast<uint8_t*>(a.out_scales + (size_t)t.nt * a.rows + row)[part] =
+        static_cast<uint8_t>(byte);
   }
 }
 
@@ -304,15 +379,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     grouped_mx_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmSB, const MxGemmArgs args) {
-  using F = Fmt<FMT>;
+  using S = Shape<FMT, EPI>;
+  constexpr int STAGES = S::kStages;
   pdl_launch_dependents();
   pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* smem_sf = smem + (size_t)STAGES * STAGE_BYTES;
-  SmemTail& st = *reinterpret_cast<SmemTail*>(smem_sf + (size_t)STAGES * F::kSf);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  SmemTail& st = *reinterpret_cast<SmemTail*>(smem + S::kOffTail);
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
@@ -338,7 +413,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&st.empty[s], 1);  // both: one commit from the leader's MMA thread
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&st.sfa_full[b], 8);   // leader: the scale warps of both CTAs
+      mbar_init(&st.sfa_full[b], 2);   // leader: the scale warps of both CTAs
       mbar_init(&st.sfa_empty[b], 1);  // both: one commit
     }
     mbar_init(&st.tfull, 1);
@@ -394,16 +469,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem_base = st.tmem_base;
+  const uint32_t tmem_base = uniform(st.tmem_base);
   const WaitCtx wc{&st.abort_flag, args.status, args.timeout_ns};
   const int k_steps = (args.k_bytes + KB - 1) / KB;
+  const int dm = nclusters / args.n_tiles, dn = nclusters - dm * args.n_tiles;
+  TileWalk walk;
+  walk.start(cluster, args.n_tiles, args.groups, st.mt_start);
 
-  if (warp < EPI_WARP0) {
-    regs_dec<REGS_ISSUE>();
+  if (warp < 3) {
     // The issuing warps run their loops with all lanes and elect one to issue, so
     // that stages, addresses and descriptors stay in uniform registers: with one
     // lane in the loop a K step took 960 cycles to issue, twice its MMAs' time.
-    const uint32_t smem0 = smem_u32(smem), sf0 = smem_u32(smem_sf);
+    const uint32_t smem0 = smem_u32(smem), sfb0 = smem0 + S::kOffSfb;
     if (warp == 0 || warp == 2) {
       // ------------------------------------------------ TMA producers (both CTAs):
       // A and B's scales, and the barrier's byte count (warp 0); B (warp 2)
@@ -413,13 +490,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       const uint32_t full0 = mapa_shared(smem_u32(&st.full[0]), 0);  // the leader's barriers
       for (int tile = cluster; ok && tile < total; tile += nclusters) {
-        const Tile t = tile_at(tile, args.n_tiles, args.groups, st.mt_start, st.row_start);
+        if (tile != cluster) walk.next(dm, dn, args.n_tiles, args.groups, st.mt_start);
+        const Tile t = walk.tile(st.mt_start, st.row_start);
         const int a_row = t.row0 + BM * (int)rank;
         const int b_row = (t.nt * args.n_out_tile + (int)rank * args.b_second) >> 2;
         const bool load_a = t.rows > BM * (int)rank;  // a half without rows loads none
         const int n0 = t.nt * args.n_out_tile, n1 = n0 + args.b_second;
         int sf_row = t.g * args.words;
-        const uint32_t tx = 2 * (B_BYTES + 2 * F::kWords * SF_BYTES) + A_BYTES +
+        const uint32_t tx = 2 * (B_BYTES + 2 * S::kWords * SF_BYTES) + A_BYTES +
                             (t.rows > BM ? A_BYTES : 0);
         int kb = 0;
         for (int ks = 0; ks < k_steps; ++ks) {
@@ -433,9 +511,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (warp == 0) {
               if (leader) mbar_arrive_expect_tx(&st.full[stage], tx);
               if (load_a) tma_load_2d_at(sa, &tmA, full, kb, a_row);
-              const uint32_t sb = sf0 + stage * F::kSf;
+              const uint32_t sb = sfb0 + stage * S::kSfb;
               tma_load_2d_at(sb, &tmSB, full, n0, sf_row);
-              tma_load_2d_at(sb + F::kWords * SF_BYTES, &tmSB, full, n1, sf_row);
+              tma_load_2d_at(sb + S::kWords * SF_BYTES, &tmSB, full, n1, sf_row);
             } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
@@ -445,7 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           kb += KB;
-          sf_row += F::kWords;
+          sf_row += S::kWords;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -459,24 +537,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     } else if (warp == 1 && leader) {
       // ------------------------------------------------ B's scales to TMEM and pair MMAs (leader)
-      constexpr int SFA_STEPS = SFA_WORDS / F::kWords;  // K steps per buffer of A's scales
+      constexpr int SFA_STEPS = SFA_WORDS / S::kWords;  // K steps per buffer of A's scales
       int stage = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0, sfa_phase = 0;
       bool ok = true;
-      const uint64_t da0 = sdesc_kmajor_sw128(smem0), dsf0 = sdesc_rows16(sf0);
+      const uint64_t da0 = sdesc_kmajor_sw128(smem0), dsfb0 = sdesc_rows16(sfb0),
+                     dsfa0 = sdesc_rows16(smem0 + S::kOffSfa);
       const int last = args.k_bytes - (k_steps - 1) * KB;  // bytes of a row in the last step
       for (int tile = cluster; ok && tile < total; tile += nclusters) {
-        if (!__all_sync(FULL, mbar_wait(&st.tempty, acc_phase ^ 1u, wc, 62))) break;
         int chunk_left = 0;
-        uint32_t sfa = 0;
+        uint64_t dsfa = dsfa0;
         for (int ks = 0; ks < k_steps; ++ks) {
           if (chunk_left == 0) {
             if (!__all_sync(FULL, mbar_wait(&st.sfa_full[buf], sfa_phase, wc, 66))) {
               ok = false;
               break;
             }
+            mbar_acquire_cluster(&st.sfa_full[buf], sfa_phase);  // the peer's words
             chunk_left = SFA_STEPS;
-            sfa = tmem_base + TMEM_SFA + 64 * buf;
+            dsfa = dsfa0 + static_cast<uint64_t>(buf * (SFA_BYTES >> 4));
           }
           if (!__all_sync(FULL, mbar_wait(&st.full[stage], phase, wc, 63))) {
             ok = false;
@@ -485,17 +564,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           tc_fence_after_sync();
           --chunk_left;
           const bool chunk_done = chunk_left == 0 || ks + 1 == k_steps;
-          const uint32_t sfb = tmem_base + TMEM_SFB + 16 * stage;
-          const uint64_t dsf = dsf0 + static_cast<uint64_t>(stage * (F::kSf >> 4));
+          const uint32_t sfa = tmem_base + TMEM_SF + 32 * stage, sfb = sfa + TMEM_SFB;
+          const uint64_t dsfb = dsfb0 + static_cast<uint64_t>(stage * (S::kSfb >> 4));
           const uint64_t da = da0 + static_cast<uint64_t>(stage * (STAGE_BYTES >> 4));
           const uint64_t db = da + (A_BYTES >> 4);
           if (elect_one()) {
 #pragma unroll
-            for (int w = 0; w < F::kWords; ++w)
+            for (int w = 0; w < S::kWords; ++w) {
+              tmem_copy_sf_pair(sfa + 4 * w, dsfa + w * (SF_BYTES >> 4));
 #pragma unroll
               for (int hb = 0; hb < 2; ++hb)
                 tmem_copy_sf_pair(sfb + 8 * w + 4 * hb,
-                                  dsf + (F::kWords * hb + w) * (SF_BYTES >> 4));
+                                  dsfb + (S::kWords * hb + w) * (SF_BYTES >> 4));
+            }
+          }
+          // the accumulator is needed only now: with the scales and operands waited for
+          // after it, the tensor cores idled 1,000 cycles more at every tile's start
+          if (ks == 0 && !__all_sync(FULL, mbar_wait(&st.tempty, acc_phase ^ 1u, wc, 62))) {
+            ok = false;
+            break;
+          }
+          if (ks == 0) tc_fence_after_sync();
+          if (elect_one()) {
             // 32 bytes of every row per MMA; the scale word, and the byte in it
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -503,13 +593,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 umma_mx_pair<FMT>(
                     tmem_base, da + 2 * kk, db + 2 * kk,
                     idesc_sf(idesc_mx<FMT>(), FMT == MOE_MXFP8 ? kk : 2 * (kk & 1)),
-                    sfa + 4 * (kk * F::kWords / 4), sfb + 8 * (kk * F::kWords / 4),
+                    sfa + 4 * (kk * S::kWords / 4), sfb + 8 * (kk * S::kWords / 4),
                     (ks | kk) != 0 ? 1u : 0u);
             umma_commit_pair_mask(&st.empty[stage], 0x3);
             if (chunk_done) umma_commit_pair_mask(&st.sfa_empty[buf], 0x3);
             if (ks + 1 == k_steps) umma_commit_pair_mask(&st.tfull, 0x3);
           }
-          sfa += 4 * F::kWords;
+          dsfa += S::kWords * (SF_BYTES >> 4);
           if (chunk_done) {
             chunk_left = 0;
             buf ^= 1;
@@ -528,87 +618,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     }
-  } else if (warp < SFA_WARP0) {
-    regs_inc<REGS_EPI>();
-    // ------------------------------------------------ epilogue warps 4..11 (both CTAs)
+  } else if (warp == 3) {
+    // ------------------------------------------------ scales of this CTA's rows of A
+    const uint32_t full_leader[2] = {mapa_shared(smem_u32(&st.sfa_full[0]), 0),
+                                     mapa_shared(smem_u32(&st.sfa_full[1]), 0)};
+    const uint32_t sfa0 = smem_u32(smem) + S::kOffSfa + 16 * lane;
+    int buf = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = cluster; ok && tile < total; tile += nclusters) {
+      if (tile != cluster) walk.next(dm, dn, args.n_tiles, args.groups, st.mt_start);
+      const Tile t = walk.tile(st.mt_start, st.row_start);
+      const int rows = min(BM, t.rows - BM * (int)rank);  // may be <= 0
+      const uint32_t* src = args.a_scales + t.row0 + BM * (int)rank + lane;
+      for (int w0 = 0; w0 < args.words; w0 += SFA_WORDS) {
+        // words of rows lane + 32 j, 8 words at a time; the first are loaded while
+        // the buffer is still in use
+        const int nw = min(SFA_WORDS, args.words - w0);
+        uint32_t v[8][4];
+        auto load = [&](int h) {
+#pragma unroll
+          for (int w = 0; w < 8; ++w)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[w][j] = h + w < nw && lane + 32 * j < rows
+                            ? src[(size_t)(w0 + h + w) * args.rows + 32 * j]
+                            : 0u;
+        };
+        auto store = [&](int h) {
+#pragma unroll
+          for (int w = 0; w < 8; ++w)
+            st_shared_v4(sfa0 + buf * SFA_BYTES + (h + w) * SF_BYTES, v[w]);
+        };
+        load(0);
+        if (!__all_sync(FULL, mbar_wait(&st.sfa_empty[buf], phase ^ 1u, wc, 65))) {
+          ok = false;
+          break;
+        }
+        store(0);
+        if (nw > 8) {
+          load(8);
+          store(8);
+        }
+        fence_proxy_async_smem();  // these writes -> tcgen05.cp
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(full_leader[buf]);
+        buf ^= 1;
+        if (buf == 0) phase ^= 1u;
+      }
+    }
+  } else {
+    // ------------------------------------------------ epilogue warps 4..19 (both CTAs)
     const int q = warp & 3;
-    const int half = (warp - EPI_WARP0) >> 2;
+    const int part = (warp - EPI_WARP0) >> 2;
     const int r_in_tile = q * 32 + lane;
     const uint32_t tempty_leader = mapa_shared(smem_u32(&st.tempty), 0);
     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t out = smem_u32(smem) + S::kOffOut;
     uint32_t acc_phase = 0;
     for (int tile = cluster; tile < total; tile += nclusters) {
-      Tile t = tile_at(tile, args.n_tiles, args.groups, st.mt_start, st.row_start);
+      if (tile != cluster) walk.next(dm, dn, args.n_tiles, args.groups, st.mt_start);
+      Tile t = walk.tile(st.mt_start, st.row_start);
       t.row0 += BM * (int)rank;
       t.rows = max(0, min(BM, t.rows - BM * (int)rank));
       const bool ok = mbar_wait(&st.tfull, acc_phase, wc, 64);
       if (!__all_sync(FULL, ok)) break;  // warp-uniform exit
       tc_fence_after_sync();
-      uint32_t v[128];
-      if constexpr (EPI == MX_SWIGLU) {
-        // accumulator columns [0,128) gate, [128,256) up; this half: output columns
-        // half*64 + [0,64), which are 16 consecutive columns of each j
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          tmem_ld_32x32b_x16(tb + 32 * j + half * 16,
-                             *reinterpret_cast<uint32_t(*)[16]>(v + 16 * j));
-          tmem_ld_32x32b_x16(tb + BN / 2 + 32 * j + half * 16,
-                             *reinterpret_cast<uint32_t(*)[16]>(v + 64 + 16 * j));
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_ld_32x32b_x32(tb + half * 128 + 32 * c,
-                             *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
-      }
-      tmem_ld_wait();
+      uint32_t v[EPI_COLS];
+      load_part<EPI>(tb, part, v);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(tempty_leader);
-      epilogue<FMT, EPI>(args, v, t, r_in_tile, half);
+      store_part<FMT, EPI>(args, v, t, r_in_tile, part, out);
       acc_phase ^= 1u;
     }
-  } else {
-    regs_dec<REGS_SFA>();
-    // ------------------------------------------------ scales of this CTA's rows of A
-    const uint32_t full_leader[2] = {mapa_shared(smem_u32(&st.sfa_full[0]), 0),
-                                     mapa_shared(smem_u32(&st.sfa_full[1]), 0)};
-    const uint32_t tq = tmem_base + TMEM_SFA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    int buf = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int tile = cluster; ok && tile < total; tile += nclusters) {
-      const Tile t = tile_at(tile, args.n_tiles, args.groups, st.mt_start, st.row_start);
-      const int rows = min(BM, t.rows - BM * (int)rank);  // may be <= 0
-      const uint32_t* src = args.a_scales + t.row0 + BM * (int)rank + lane;
-      for (int w0 = 0; w0 < args.words; w0 += SFA_WORDS) {
-        const bool got = mbar_wait(&st.sfa_empty[buf], phase ^ 1u, wc, 65);
-        if (!__all_sync(FULL, got)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const int nw = min(SFA_WORDS, args.words - w0);
-#pragma unroll 1
-        for (int h = 0; h < nw; h += 8) {  // 8 words of rows lane + 32 j: column 4 w + j
-          uint32_t v[32];
-#pragma unroll
-          for (int w = 0; w < 8; ++w)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v[4 * w + j] = h + w < nw && lane + 32 * j < rows
-                                 ? src[(size_t)(w0 + h + w) * args.rows + 32 * j]
-                                 : 0u;
-          tmem_st_32x32b_x32(tq + 64 * buf + 4 * h, v);
-        }
-        tmem_st_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(full_leader[buf]);
-        buf ^= 1;
-        if (buf == 0) phase ^= 1u;
-      }
-    }
+    // the last tile's copies have left shared memory and are written
+    if constexpr (EPI == MX_ROWS) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   // both CTAs are done with the accumulator and the scales before either frees TMEM or exits
@@ -679,7 +764,7 @@ cudaError_t make_tmap_sb(CUtensorMap* map, const void* base, uint64_t word_rows,
 template <int FMT, int EPI>
 cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSB,
                    const MxGemmArgs& args, int grid, cudaStream_t stream) {
-  constexpr size_t smem = Fmt<FMT>::kSmem + sizeof(SmemTail);
+  constexpr size_t smem = 1024 + Shape<FMT, EPI>::kOffTail + sizeof(SmemTail);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<int> smem_set[MAX_DEVICES];
   const cudaError_t e =
