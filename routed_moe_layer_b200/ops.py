@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -536,22 +537,33 @@ def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _is(t, name: str, dtype, shape: Sequence[int]):
+    """_need for the calls whose host time counts: one test when all is well."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+
+
 def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
+    dev = first.device
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
-    return first.device
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+    return dev
 
 
 def _call(name: str, dev: torch.device, *args):
     """Calls entry point ``name`` with dev current, on dev's current stream."""
-    fn = getattr(lib(), name)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, stream), name)
+    fn = getattr(_lib or lib(), name)
+    # what torch.cuda.current_stream(dev).cuda_stream reads, without the Stream object
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if dev.index == torch._C._cuda_getDevice():
+        code = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream), name)
+            code = fn(*args, stream)
+    if code != MOE_OK:
+        _check(code, name)
 
 
 def mx_words(K: int) -> int:
@@ -559,10 +571,16 @@ def mx_words(K: int) -> int:
     return (K + 127) // 128
 
 
+@functools.lru_cache(maxsize=256)
+def _ws_bytes(name: str, *sizes: int) -> int:
+    """Bytes of a workspace (the least one where the sizes are refused, as the call then is)."""
+    return max(int(getattr(lib(), name)(*sizes)), 256)
+
+
 def _need_mx(codes: torch.Tensor, scales: torch.Tensor, name: str, lead: Sequence[int], rows: int,
              K: int, fmt: int):
-    _need(codes, f"{name}_codes", torch.uint8, (*lead, rows, K if fmt == 1 else K // 2))
-    _need(scales, f"{name}_scales", torch.uint8, (*lead, mx_words(K), rows, 4))
+    _is(codes, f"{name}_codes", torch.uint8, (*lead, rows, K if fmt == 1 else K // 2))
+    _is(scales, f"{name}_scales", torch.uint8, (*lead, mx_words(K), rows, 4))
 
 
 def _matrices(t: torch.Tensor, name: str):
@@ -577,9 +595,10 @@ def mx_quantize(x: torch.Tensor, fmt: str):
     """(codes, scales) of bf16 x [rows, K] or [G, rows, K] (moe_mx_quantize)."""
     f = _fmt(fmt)
     G, lead, rows, K = _matrices(x, "x")
-    _need(x, "x", torch.bfloat16, (*lead, rows, K))
-    codes = torch.empty((*lead, rows, K if f == 1 else K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((*lead, mx_words(K), rows, 4), dtype=torch.uint8, device=x.device)
+    _is(x, "x", torch.bfloat16, (*lead, rows, K))
+    codes = (torch.empty_like(x, dtype=torch.uint8) if f == 1 else
+             x.new_empty((*lead, rows, K // 2), dtype=torch.uint8))
+    scales = x.new_empty((*lead, mx_words(K), rows, 4), dtype=torch.uint8)
     _call("moe_mx_quantize", x.device, x.data_ptr(), G, rows, K, f, codes.data_ptr(),
           scales.data_ptr())
     return codes, scales
@@ -592,7 +611,7 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: str) -> torch.
     K = K if f == 1 else 2 * K
     _need_mx(codes, scales, "x", lead, rows, K, f)
     dev = _one_device(codes, scales)
-    x = torch.empty((*lead, rows, K), dtype=torch.bfloat16, device=dev)
+    x = codes.new_empty((*lead, rows, K), dtype=torch.bfloat16)
     _call("moe_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), G, rows, K, f,
           x.data_ptr())
     return x
@@ -609,14 +628,14 @@ def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     T, H = x.shape
-    _need(x, "x", torch.bfloat16, (T, H))
+    _is(x, "x", torch.bfloat16, (T, H))
     f = 0 if fmt is None else _fmt(fmt)
     if residual is not None:
-        _need(residual, "residual", torch.bfloat16, (T, H))
+        _is(residual, "residual", torch.bfloat16, (T, H))
     if gamma is not None:
-        _need(gamma, "gamma", torch.float32, (H,))
+        _is(gamma, "gamma", torch.float32, (H,))
     if sum_out is not None:
-        _need(sum_out, "sum_out", torch.bfloat16, (T, H))
+        _is(sum_out, "sum_out", torch.bfloat16, (T, H))
     dev = _one_device(x, residual, gamma, sum_out)
     total = sum_out
     if total is None:
@@ -624,8 +643,9 @@ def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
     xn = torch.empty_like(x)
     codes = scales = None
     if f:
-        codes = torch.empty((T, H if f == 1 else H // 2), dtype=torch.uint8, device=dev)
-        scales = torch.empty((mx_words(H), T, 4), dtype=torch.uint8, device=dev)
+        codes = (torch.empty_like(x, dtype=torch.uint8) if f == 1 else
+                 x.new_empty((T, H // 2), dtype=torch.uint8))
+        scales = x.new_empty((mx_words(H), T, 4), dtype=torch.uint8)
     _call("moe_add_rmsnorm", dev, x.data_ptr(), _at(residual), _at(gamma), float(eps), T, H, f,
           None if total is x and residual is None else total.data_ptr(), xn.data_ptr(),
           _at(codes), _at(scales))
@@ -644,16 +664,17 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
         raise ValueError("x must be a matrix and w a stack of matrices")
     R, K = x.shape
     E, N, _ = w.shape
-    _need(x, "x", torch.bfloat16, (R, K))
-    _need(w, "w", torch.bfloat16, (E, N, K))
-    _need(offsets, "offsets", torch.int32, (E + 1,))
+    _is(x, "x", torch.bfloat16, (R, K))
+    _is(w, "w", torch.bfloat16, (E, N, K))
+    _is(offsets, "offsets", torch.int32, (E + 1,))
     if out is None:
-        out = torch.empty((R, N), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((R, N))
     else:
-        _need(out, "out", torch.bfloat16, (R, N))
+        _is(out, "out", torch.bfloat16, (R, N))
     dev = _one_device(x, w, offsets, out, workspace)
     if workspace is None:
-        workspace = alloc_workspace(lib().moe_grouped_mm_workspace_bytes(R, E, N, K), dev)
+        workspace = x.new_empty(_ws_bytes("moe_grouped_mm_workspace_bytes", R, E, N, K),
+                                dtype=torch.uint8)
     _call("moe_grouped_mm", dev, x.data_ptr(), offsets.data_ptr(), R, E, N, K, w.data_ptr(),
           out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
@@ -661,15 +682,15 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
 
 def _mx_out(R: int, N: int, dev, row_w, row_dest, out, out_rows):
     if row_w is not None:
-        _need(row_w, "row_w", torch.float32, (R,))
+        _is(row_w, "row_w", torch.float32, (R,))
     if row_dest is not None:
-        _need(row_dest, "row_dest", torch.int32, (R,))
+        _is(row_dest, "row_dest", torch.int32, (R,))
     if out is None:
         return torch.empty((R if out_rows is None else out_rows, N), dtype=torch.bfloat16,
                            device=dev)
     if out_rows is None:
         out_rows = out.shape[0] if isinstance(out, torch.Tensor) and out.dim() == 2 else R
-    _need(out, "out", torch.bfloat16, (out_rows, N))
+    _is(out, "out", torch.bfloat16, (out_rows, N))
     return out
 
 
@@ -689,11 +710,11 @@ def grouped_mm_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.
     K = kb if f == 1 else 2 * kb
     _need_mx(x_codes, x_scales, "x", (), R, K, f)
     _need_mx(w_codes, w_scales, "w", (E,), N, K, f)
-    _need(offsets, "offsets", torch.int32, (E + 1,))
+    _is(offsets, "offsets", torch.int32, (E + 1,))
     y = _mx_out(R, N, x_codes.device, row_w, row_dest, out, out_rows)
     dev = _one_device(x_codes, x_scales, w_codes, w_scales, offsets, row_w, row_dest, y, workspace)
     if workspace is None:
-        workspace = alloc_workspace(256, dev)
+        workspace = y.new_empty(256, dtype=torch.uint8)
     _call("moe_grouped_mm_mx", dev, x_codes.data_ptr(), x_scales.data_ptr(), offsets.data_ptr(), R,
           E, N, K, f, w_codes.data_ptr(), w_scales.data_ptr(), _at(row_w), _at(row_dest),
           y.data_ptr(), y.shape[0], workspace.data_ptr(), workspace.numel())
@@ -719,17 +740,17 @@ def expert_rows_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, offsets: torch
     _need_mx(x_codes, x_scales, "x", (), T, H, f)
     _need_mx(w13_codes, w13_scales, "w13", (E,), 2 * I, H, f)
     _need_mx(w2_codes, w2_scales, "w2", (E,), H, I, f)
-    _need(offsets, "offsets", torch.int32, (E + 1,))
+    _is(offsets, "offsets", torch.int32, (E + 1,))
     R = T
     if tok_of is not None:
         R = tok_of.numel()
-        _need(tok_of, "tok_of", torch.int32, (R,))
+        _is(tok_of, "tok_of", torch.int32, (R,))
     y = _mx_out(R, H, x_codes.device, row_w, row_dest, y, y_rows)
     dev = _one_device(x_codes, x_scales, offsets, w13_codes, w13_scales, w2_codes, w2_scales,
                       row_dest, row_w, tok_of, y, workspace)
     if workspace is None:
-        workspace = alloc_workspace(lib().moe_expert_rows_mx_workspace_bytes(
-            R, H, E, I, f, int(tok_of is not None)), dev)
+        workspace = y.new_empty(_ws_bytes("moe_expert_rows_mx_workspace_bytes", R, H, E, I, f,
+                                          int(tok_of is not None)), dtype=torch.uint8)
     _call("moe_expert_rows_mx", dev, x_codes.data_ptr(), x_scales.data_ptr(), T, _at(tok_of),
           offsets.data_ptr(), R, E, H, I, f, w13_codes.data_ptr(), w13_scales.data_ptr(),
           w2_codes.data_ptr(), w2_scales.data_ptr(), _at(row_w), _at(row_dest), y.data_ptr(),
