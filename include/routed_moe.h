@@ -367,8 +367,9 @@ MOE_API int32_t moe_rmsnorm(const void* x, const float* gamma, float eps, int32_
  *           [b/4][r][b%4]; bytes of blocks past K must be 0
  * A stack of matrices [G, rows, K] has G such arrays of each, one after the
  * other.  K is a multiple of 32 (<= 16384).  codes, bf16 inputs, xn and
- * the scales of weights are 16-byte aligned, bf16 outputs of products 32-byte,
- * the scales of rows 4-byte (MOE_ERR_INVALID_ARG).  Forward only, like the block itself. */
+ * the scales of weights are 16-byte aligned, bf16 outputs of products and what
+ * is quantised or dequantised 32-byte, the scales of rows 4-byte
+ * (MOE_ERR_INVALID_ARG).  Forward only, like the block itself. */
 typedef enum {
   MOE_MXFP8 = 1, /* E4M3 elements */
   MOE_MXFP4 = 2  /* E2M1 elements */
@@ -378,7 +379,7 @@ typedef enum {
  * at least -127 (no element saturates); elements are rounded once, to nearest,
  * ties to the even code.  A block that holds a NaN or an infinity gets the
  * scale byte 255 (NaN) and codes 0: every product with it is NaN.
- *   x      device bf16 [groups, rows, K]
+ *   x      device bf16 [groups, rows, K], groups * rows < 2^30
  *   codes, scales  out, as above (bytes of blocks past K are written as 0) */
 MOE_API int32_t moe_mx_quantize(const void* x, int32_t groups, int32_t rows, int32_t K,
                                 int32_t fmt, uint8_t* codes, uint8_t* scales, void* stream);

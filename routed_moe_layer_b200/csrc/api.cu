@@ -660,7 +660,8 @@ bool mx_fmt_ok(int32_t fmt) { return fmt == MOE_MXFP8 || fmt == MOE_MXFP4; }
 // A matrix of rows x K elements, or a stack of them.
 int32_t check_mx(int32_t groups, int32_t rows, int32_t K, int32_t fmt) {
   if (groups < 0 || rows < 0 || K <= 0 || !mx_fmt_ok(fmt)) return MOE_ERR_INVALID_ARG;
-  if (K % 32 != 0 || K > MAX_DIM) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (K % 32 != 0 || K > MAX_DIM || (int64_t)groups * rows > INT32_MAX / 2)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
 
@@ -1115,7 +1116,7 @@ int32_t moe_mx_quantize(const void* x, int32_t groups, int32_t rows, int32_t K, 
   if (st != MOE_OK) return st;
   if (groups == 0 || rows == 0) return MOE_OK;
   if (!x || !codes || !scales || codes == x) return MOE_ERR_INVALID_ARG;
-  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 32) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_mx_quantize(x, groups, rows, K, fmt, codes, scales,
                                         static_cast<cudaStream_t>(stream)));
 }
@@ -1126,7 +1127,7 @@ int32_t moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t g
   if (st != MOE_OK) return st;
   if (groups == 0 || rows == 0) return MOE_OK;
   if (!x || !codes || !scales || codes == x) return MOE_ERR_INVALID_ARG;
-  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 32) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_mx_dequantize(codes, scales, groups, rows, K, fmt, x,
                                           static_cast<cudaStream_t>(stream)));
 }

@@ -774,28 +774,44 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
                         tmB, tmSB, args);
 }
 
-// Rows of narrow tokens in expert order: codes[r] = tokens[tok_of[r]] (16-byte
-// vectors) and the words of scales; a token outside [0, T) gives zeros.
+// Rows of narrow tokens in expert order: codes[r] = tokens[tok_of[r]] and the
+// words of scales; a token outside [0, T) gives zeros.  A block takes 32 rows, a
+// warp four of them, whose 512-byte pieces are in flight together.  Bound by the
+// writes: 155,296 rows of 2,048 bytes are 318 MB, 81 us at the 3.9 TB/s that
+// writes alone reach here.
+constexpr int GATHER_ROWS = 32;
+
 __global__ void __launch_bounds__(256)
     gather_mx_kernel(const uint4* __restrict__ codes, const uint32_t* __restrict__ scales,
                      const int* __restrict__ tok_of, int T, int R, int vecs, int words,
                      uint4* __restrict__ codes_out, uint32_t* __restrict__ scales_out) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long step = (long long)gridDim.x * blockDim.x;
-  const long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  for (long long i = i0; i < (long long)R * vecs; i += step) {
-    const int r = (int)(i / vecs);
-    const int c = (int)(i - (long long)r * vecs);
-    const int t = tok_of[r];
-    codes_out[i] = t >= 0 && t < T ? codes[(size_t)t * vecs + c] : make_uint4(0, 0, 0, 0);
+  __shared__ int tok[GATHER_ROWS];
+  const int row0 = blockIdx.x * GATHER_ROWS;
+  const int rows = min(GATHER_ROWS, R - row0);
+  if (threadIdx.x < GATHER_ROWS) {
+    const int t = (int)threadIdx.x < rows ? tok_of[row0 + threadIdx.x] : -1;
+    tok[threadIdx.x] = t >= 0 && t < T ? t : -1;
   }
-  for (long long i = i0; i < (long long)R * words; i += step) {
-    const int w = (int)(i / R);
-    const int r = (int)(i - (long long)w * R);
-    const int t = tok_of[r];
-    scales_out[i] = t >= 0 && t < T ? scales[(size_t)w * T + t] : 0u;
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int c = lane; c < vecs; c += 32) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = tok[warp * 4 + j];
+      v[j] = t >= 0 ? codes[(size_t)t * vecs + c] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (warp * 4 + j < rows) codes_out[(size_t)(row0 + warp * 4 + j) * vecs + c] = v[j];
   }
+  for (int w = warp; w < words; w += 8)
+    if (lane < rows) {
+      const int t = tok[lane];
+      scales_out[(size_t)w * R + row0 + lane] = t >= 0 ? scales[(size_t)w * T + t] : 0u;
+    }
 }
 
 }  // namespace
@@ -827,10 +843,8 @@ cudaError_t launch_gather_mx(const uint8_t* codes, const uint8_t* scales, const 
                              int R, int row_bytes, int words, uint8_t* codes_out,
                              uint8_t* scales_out, cudaStream_t stream) {
   const int vecs = row_bytes / 16;
-  long long blocks = ((long long)R * vecs + 255) / 256;
-  const long long cap = (long long)num_sms() * 8;
-  if (blocks > cap) blocks = cap;
-  return launch_chained(gather_mx_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
+  const unsigned blocks = (R + GATHER_ROWS - 1) / GATHER_ROWS;
+  return launch_chained(gather_mx_kernel, dim3(blocks), dim3(256), 0, stream,
                         reinterpret_cast<const uint4*>(codes),
                         reinterpret_cast<const uint32_t*>(scales), tok_of, T, R, vecs, words,
                         reinterpret_cast<uint4*>(codes_out),

@@ -28,6 +28,7 @@ def L():
     ({"x": 0}, INVALID), ({"codes": 0}, INVALID), ({"scales": 0}, INVALID),
     ({"x": P + 8}, INVALID), ({"codes": 2 * P + 4}, INVALID), ({"scales": 3 * P + 2}, INVALID),
     ({"codes": P}, INVALID),  # in place
+    ({"x": P + 16}, INVALID), ({"groups": 2 ** 20, "rows": 2 ** 12}, SHAPE),
 ])
 def test_quantize_checks(L, kw, expect):
     a = dict(x=P, groups=1, rows=4, K=64, fmt=1, codes=2 * P, scales=3 * P) | kw
