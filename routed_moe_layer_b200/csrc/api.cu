@@ -691,6 +691,13 @@ MxGemmArgs mx_args(const uint8_t* a_scales, const int32_t* offsets, int32_t R, i
   return g;
 }
 
+// At most 64 rows per group on average: the operands swapped (as use_swap).
+cudaError_t mx_product(int fmt, int epi, const void* a, const void* b, const MxGemmArgs& g,
+                       cudaStream_t s) {
+  return (int64_t)g.rows <= 64LL * g.groups ? launch_grouped_mx_few(fmt, epi, a, b, g, s)
+                                            : launch_grouped_mx(fmt, epi, a, b, g, s);
+}
+
 struct MxExpertsLayout {
   size_t x, xs, h, hs, total;
 };
@@ -1218,8 +1225,8 @@ int32_t moe_grouped_mm_mx(const uint8_t* x_codes, const uint8_t* x_scales, const
   g.out_rows = y_rows;
   g.out = y;
   g.clear_status = 1;
-  return cuda_status(launch_grouped_mx(fmt, MX_ROWS, x_codes, w_codes, g,
-                                       static_cast<cudaStream_t>(stream)));
+  return cuda_status(mx_product(fmt, MX_ROWS, x_codes, w_codes, g,
+                                static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_expert_rows_mx_workspace_bytes(int32_t R, int32_t H, int32_t E, int32_t I, int32_t fmt,
@@ -1268,7 +1275,7 @@ int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int3
   up.out = h;
   up.out_scales = reinterpret_cast<uint32_t*>(hs);
   up.clear_status = 1;
-  RMOE_TRY(launch_grouped_mx(fmt, MX_SWIGLU, a, w13_codes, up, s));
+  RMOE_TRY(mx_product(fmt, MX_SWIGLU, a, w13_codes, up, s));
   MxGemmArgs dn = mx_args(hs, offsets, R, E, I, fmt, w2_scales, status);
   dn.n_rows = H;
   dn.n_valid = H;
@@ -1276,7 +1283,7 @@ int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int3
   dn.row_dest = row_dest;
   dn.out_rows = y_rows;
   dn.out = y;
-  return cuda_status(launch_grouped_mx(fmt, MX_ROWS, h, w2_codes, dn, s));
+  return cuda_status(mx_product(fmt, MX_ROWS, h, w2_codes, dn, s));
 }
 
 int32_t moe_read_device_status(void* workspace, int32_t* site, void* stream) {

@@ -41,13 +41,7 @@
 // scales); the epilogue reads it whole into registers and hands it back before
 // it computes or stores anything.
 // Every wait is bounded (common.cuh).
-#include <mutex>
-
-#include <cudaTypedefs.h>
-
-#include "common.cuh"
-#include "kernels.h"
-#include "mx_format.cuh"
+#include "mx_mma.cuh"
 
 namespace rmoe {
 
@@ -62,7 +56,7 @@ constexpr int A_BYTES = BM * KB;
 constexpr int B_BYTES = BN / 2 * KB;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int B_BOX = 32;        // B rows per TMA box (every fourth row of the matrix)
-constexpr int SF_BYTES = 512;    // scale words of 128 rows
+constexpr int SF_BYTES = MX_SF_BYTES;
 constexpr int THREADS = 640;
 constexpr int EPI_WARP0 = 4;
 constexpr int EPI_WARPS = 16;
@@ -70,11 +64,9 @@ constexpr int EPI_COLS = 64;     // accumulator columns of an epilogue thread
 constexpr int OUT_PITCH = BN * 2 + 16;  // bytes of an output row in shared memory (no conflicts)
 constexpr int SFA_WORDS = 16;    // words per row in a buffer of A's scales
 constexpr int SFA_BYTES = SFA_WORDS * SF_BYTES;
-constexpr int MAX_GROUPS = 128;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TMEM_SF = 256;        // + 32 per stage: A, 4 per word, ...
 constexpr uint32_t TMEM_SFB = 8;         // ... B, 8 per word, 4 per half
-constexpr unsigned FULL = 0xffffffffu;
 
 template <int FMT, int EPI>
 struct Shape {
@@ -97,70 +89,8 @@ struct __align__(8) SmemTail {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  int bad_offsets;
-  int mt_start[MAX_GROUPS + 1];
-  int row_start[MAX_GROUPS + 1];
+  MxGroups groups;
 };
-
-__device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity,
-                                                uint64_t timeout_ns) {
-  const uint32_t a = smem_u32(bar);
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (globaltimer_ns() - t0 > timeout_ns) return;
-  }
-}
-
-// A value that is the same in all lanes, told to the compiler, which then keeps
-// it (and branches on it) in uniform registers.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(FULL, v, 0); }
-
-struct Tile {
-  int g, row0, rows, nt;
-};
-
-// The tiles of one cluster in order: every nclusters-th, columns fastest.  The
-// warp finds the next one's group together (32 groups a look), since a search
-// by one thread, seven dependent loads, cost each role 1,300 cycles a tile.
-struct TileWalk {
-  int g, mt, nt;
-
-  __device__ __forceinline__ void start(int tile, int n_tiles, int groups, const int* mts) {
-    mt = tile / n_tiles;
-    nt = tile - mt * n_tiles;
-    g = 0;
-    seek(groups, mts);
-  }
-  __device__ __forceinline__ void next(int dm, int dn, int n_tiles, int groups, const int* mts) {
-    mt += dm;
-    nt += dn;
-    if (nt >= n_tiles) {
-      nt -= n_tiles;
-      ++mt;
-    }
-    seek(groups, mts);
-  }
-  // largest g with mts[g] <= mt (skips empty groups); g is never past it
-  __device__ __forceinline__ void seek(int groups, const int* mts) {
-    unsigned b;
-    do {
-      const int i = min(g + (int)(threadIdx.x & 31), groups);
-      b = __ballot_sync(FULL, mts[i] <= mt && i < groups);
-      g += __popc(b) - 1;
-    } while (b == FULL);
-  }
-  __device__ __forceinline__ Tile tile(const int* mts, const int* rs) const {
-    Tile t;
-    t.g = g;
-    t.nt = nt;
-    t.row0 = uniform(rs[g] + (mt - mts[g]) * TILE_M);
-    t.rows = min(TILE_M, uniform(rs[g + 1]) - t.row0);
-    return t;
-  }
-};
-
-// The same expression as in the bf16 kernels.
-__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 // Block-scaled pair MMA.  Element and scale formats in idesc: A and B E4M3
 // with one scale per 32 of K = 32 (MXFP8), or E2M1 with two of K = 64 (MXFP4).
@@ -183,46 +113,11 @@ __device__ __forceinline__ void umma_mx_pair(uint32_t d, uint64_t a, uint64_t b,
         : "memory");
 }
 
-// Instruction descriptor without the scale ids: UE8M0 scales, M = 256, N = 256.
-template <int FMT>
-__device__ constexpr uint32_t idesc_mx() {
-  return (FMT == MOE_MXFP4 ? (1u << 7) | (1u << 10) : 0u)  // E2M1 (0: E4M3)
-         | (static_cast<uint32_t>(BN >> 3) << 17) | (1u << 23) |
-         (static_cast<uint32_t>(TILE_M >> 4) << 24);
-}
-
-// MMA kk of a K step uses scale byte kk (MXFP8) or bytes 2*(kk%2).. (MXFP4).
-__device__ __forceinline__ uint32_t idesc_sf(uint32_t idesc, uint32_t id) {
-  return idesc | (id << 4) | (id << 29);
-}
-
 // 32 rows of 16 bytes to 4 TMEM columns, repeated in the four lane quarters, in
 // both CTAs of the pair from the same shared-memory offset.
 __device__ __forceinline__ void tmem_copy_sf_pair(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
                : "memory");
-}
-
-// Unswizzled rows of 16 bytes: 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_rows16(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
-         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3])
-               : "memory");
-}
-
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(p));
-  return p != 0;
 }
 
 // Tile loads to a shared-memory address, completion counted on the barrier at
@@ -262,10 +157,6 @@ __device__ __forceinline__ void mbar_acquire_cluster(uint64_t* bar, uint32_t par
       : "memory");
 }
 
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // 32 TMEM lanes x 8 consecutive 32-bit columns.
 __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
@@ -299,6 +190,22 @@ __device__ __forceinline__ void load_part(uint32_t tb, int part, uint32_t (&v)[E
 // Named barrier of the four epilogue warps that share a TMEM lane quarter.
 __device__ __forceinline__ void quarter_sync(int q) {
   asm volatile("bar.sync %0, 128;" ::"r"(q + 1) : "memory");
+}
+
+// Whether a tile's wait has come to its end in all the epilogue warps that work
+// together (MX_ROWS: those of a quarter, which share barriers): they leave the
+// tile loop together when it has run out in one.
+template <int EPI>
+__device__ __forceinline__ bool epilogue_agrees(int q, bool ok) {
+  if constexpr (EPI == MX_SWIGLU) return ok;
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, r;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "bar.red.and.pred r, %1, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}\n"
+      : "=r"(all)
+      : "r"(q + 1), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return all != 0;
 }
 
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
@@ -392,21 +299,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const bool leader = rank == 0;
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
 
-  // group table; offsets that run backwards or past the rows are cut to the
-  // rows, so that no access leaves the operands, and reported
-  if (threadIdx.x == 0) {
-    st.bad_offsets = 0;
-    if (blockIdx.x == 0 && args.clear_status) {
-      args.status[0] = 0;
-      args.status[1] = 0;
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i <= args.groups; i += THREADS) {
-    const int o = args.offsets[i];
-    st.row_start[i] = min(max(o, 0), args.rows);
-    if (o < 0 || o > args.rows || (i > 0 && o < args.offsets[i - 1])) st.bad_offsets = 1;
-  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&st.full[s], 1);   // leader: its producer's expect-tx arrive
@@ -427,38 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmSB);
   }
-  __syncthreads();
-  if (threadIdx.x == 0 && blockIdx.x == 0 && st.bad_offsets)
-    report_error(args.status, MOE_ERR_DEVICE_INDEX, 60);
-  if (warp == 0) {  // exclusive prefix of tiles over groups (4 groups per lane)
-    constexpr int PER = MAX_GROUPS / 32;
-    int loc[PER], sum = 0;
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const int g = lane * PER + q;
-      loc[q] =
-          g < args.groups
-              ? (max(st.row_start[g + 1] - st.row_start[g], 0) + TILE_M - 1) / TILE_M
-              : 0;
-      sum += loc[q];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(FULL, incl, off);
-      if (lane >= off) incl += u;
-    }
-    int run = incl - sum;
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const int g = lane * PER + q;
-      if (g < args.groups) st.mt_start[g] = run;
-      run += loc[q];
-    }
-    if (lane == 31) st.mt_start[args.groups] = incl;
-  }
-  __syncthreads();
-  const int total = st.mt_start[args.groups] * args.n_tiles;
+  const int total = mx_group_table<TILE_M, THREADS>(args, st.groups) * args.n_tiles;
   if (cluster >= total) return;  // the same for both CTAs of the cluster; nothing allocated yet
   cluster_sync();                // both CTAs' barriers exist before any cross-CTA traffic
 
@@ -473,8 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const WaitCtx wc{&st.abort_flag, args.status, args.timeout_ns};
   const int k_steps = (args.k_bytes + KB - 1) / KB;
   const int dm = nclusters / args.n_tiles, dn = nclusters - dm * args.n_tiles;
-  TileWalk walk;
-  walk.start(cluster, args.n_tiles, args.groups, st.mt_start);
+  TileWalk<TILE_M> walk;
+  walk.start(cluster, args.n_tiles, args.groups, st.groups.mt_start);
 
   if (warp < 3) {
     // The issuing warps run their loops with all lanes and elect one to issue, so
@@ -490,8 +351,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       const uint32_t full0 = mapa_shared(smem_u32(&st.full[0]), 0);  // the leader's barriers
       for (int tile = cluster; ok && tile < total; tile += nclusters) {
-        if (tile != cluster) walk.next(dm, dn, args.n_tiles, args.groups, st.mt_start);
-        const Tile t = walk.tile(st.mt_start, st.row_start);
+        if (tile != cluster) walk.next(dm, dn, args.n_tiles, args.groups, st.groups.mt_start);
+        const Tile t = walk.tile(st.groups.mt_start, st.groups.row_start);
         const int a_row = t.row0 + BM * (int)rank;
         const int b_row = (t.nt * args.n_out_tile + (int)rank * args.b_second) >> 2;
         const bool load_a = t.rows > BM * (int)rank;  // a half without rows loads none
@@ -592,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               if (ks + 1 < k_steps || kk * 32 < last)
                 umma_mx_pair<FMT>(
                     tmem_base, da + 2 * kk, db + 2 * kk,
-                    idesc_sf(idesc_mx<FMT>(), FMT == MOE_MXFP8 ? kk : 2 * (kk & 1)),
+                    idesc_sf(idesc_mx<FMT>(TILE_M, BN), FMT == MOE_MXFP8 ? kk : 2 * (kk & 1)),
                     sfa + 4 * (kk * S::kWords / 4), sfb + 8 * (kk * S::kWords / 4),
                     (ks | kk) != 0 ? 1u : 0u);
             umma_commit_pair_mask(&st.empty[stage], 0x3);
@@ -627,8 +488,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int tile = cluster; ok && tile < total; tile += nclusters) {
-      if (tile != cluster) walk.next(dm, dn, args.n_tiles, args.groups, st.mt_start);
-      const Tile t = walk.tile(st.mt_start, st.row_start);
+      if (tile != cluster) walk.next(dm, dn, args.n_tiles, args.groups, st.groups.mt_start);
+      const Tile t = walk.tile(st.groups.mt_start, st.groups.row_start);
       const int rows = min(BM, t.rows - BM * (int)rank);  // may be <= 0
       const uint32_t* src = args.a_scales + t.row0 + BM * (int)rank + lane;
       for (int w0 = 0; w0 < args.words; w0 += SFA_WORDS) {
@@ -677,12 +538,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t out = smem_u32(smem) + S::kOffOut;
     uint32_t acc_phase = 0;
     for (int tile = cluster; tile < total; tile += nclusters) {
-      if (tile != cluster) walk.next(dm, dn, args.n_tiles, args.groups, st.mt_start);
-      Tile t = walk.tile(st.mt_start, st.row_start);
+      if (tile != cluster) walk.next(dm, dn, args.n_tiles, args.groups, st.groups.mt_start);
+      Tile t = walk.tile(st.groups.mt_start, st.groups.row_start);
       t.row0 += BM * (int)rank;
       t.rows = max(0, min(BM, t.rows - BM * (int)rank));
-      const bool ok = mbar_wait(&st.tfull, acc_phase, wc, 64);
-      if (!__all_sync(FULL, ok)) break;  // warp-uniform exit
+      const bool ok = __all_sync(FULL, mbar_wait(&st.tfull, acc_phase, wc, 64));
+      if (!epilogue_agrees<EPI>(q, ok)) break;
       tc_fence_after_sync();
       uint32_t v[EPI_COLS];
       load_part<EPI>(tb, part, v);
@@ -706,39 +567,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
-                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-                   CUtensorMapSwizzle swizzle) {
-  auto fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r =
-      fn(map, type, rank, const_cast<void*>(base), dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // Rows of codes in boxes of 128 bytes x 128 rows; bytes past a row's end and
 // rows past the last one read 0.
 cudaError_t make_tmap_a(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes) {
   const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
   const cuuint32_t box[2] = {KB, BM};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -748,7 +582,7 @@ cudaError_t make_tmap_b(CUtensorMap* map, const void* base, uint64_t groups, uin
   const cuuint64_t dims[4] = {row_bytes, 4, rows / 4, groups};
   const cuuint64_t strides[3] = {row_bytes, 4 * row_bytes, rows * row_bytes};
   const cuuint32_t box[4] = {KB, 1, B_BOX, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box,
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box,
                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -757,7 +591,7 @@ cudaError_t make_tmap_sb(CUtensorMap* map, const void* base, uint64_t word_rows,
                          uint32_t step_words) {
   const cuuint64_t dims[2] = {rows, word_rows}, strides[1] = {rows * 4};
   const cuuint32_t box[2] = {BM, step_words};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, base, dims, strides, box,
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, base, dims, strides, box,
                 CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
@@ -818,7 +652,7 @@ __global__ void __launch_bounds__(256)
 
 cudaError_t launch_grouped_mx(int fmt, int epi, const void* a, const void* b, MxGemmArgs args,
                               cudaStream_t stream) {
-  if (args.groups > MAX_GROUPS) return cudaErrorInvalidValue;
+  if (args.groups > MX_MAX_GROUPS) return cudaErrorInvalidValue;
   CUtensorMap tmA, tmB, tmSB;
   cudaError_t e;
   if ((e = make_tmap_a(&tmA, a, args.rows, args.k_bytes)) != cudaSuccess) return e;

@@ -1,0 +1,468 @@
+// Grouped products of MX operands for few rows per group: the product of
+// grouped_mx.cu with its operands swapped, D^T = W . X^T.
+//
+// With 15 rows an expert a 256-row tile spends its MMA time on padding and its
+// tile's fixed costs on little work, and the weights' stream, which bounds such
+// a call, waits for both.  Here 128 weight rows fill the MMA's M and at most 64
+// rows of a group its N (a multiple of 16), so that an MMA takes a quarter of
+// the time or less; one CTA per SM works alone, with 128 KB of weights in
+// flight and two accumulators.
+//
+// Work item = (chunk of at most 64 rows of one group, 128 weight rows):
+//   MX_ROWS    out[dest(r), n0 + l] = bf16( row_w[r] * D[l, r] )
+//   MX_SWIGLU  gate rows i0.. and up rows I + i0.. of the weights in two
+//              accumulators: lane l has gate and up of output column i0 + l; the
+//              32 lanes of a warp are one block of h, its largest element by a
+//              warp reduction.
+// Scales: both operands' words come by plain loads into the order that
+// tcgen05.cp wants (mx_mma.cuh), 8 words a row at a time, two buffers.
+// Warp roles: warp 0 TMA loads; warp 1 TMEM, scales to TMEM, MMAs; warp 2 the
+// weights' scales (of the gate rows), warp 3 those of the up rows and of the
+// rows; warps 4..7 the epilogue.  Every wait is bounded (common.cuh).
+#include "mx_mma.cuh"
+
+namespace rmoe {
+
+namespace {
+
+constexpr int WM = 128;           // weight rows per item (the MMA's M)
+constexpr int CHUNK = 64;         // rows per item (the MMA's N, padded to 16)
+constexpr int KB = 128;           // bytes of a row per K step
+constexpr int XBOX = 32;          // rows per TMA box
+constexpr int W_BYTES = WM * KB;
+constexpr int X_BYTES = CHUNK * KB;
+constexpr int THREADS = 256;
+constexpr int EPI_WARP0 = 4;
+constexpr int EPI_WARPS = 4;
+constexpr int SF_WORDS = 8;       // words per row in a buffer of scales
+constexpr int MAX_STAGES = 8;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t ACC_COLS = 128;   // per accumulator buffer: (gate,) up or rows, 64 each
+constexpr uint32_t TMEM_SF = 256;    // + 32 per stage: 4 per word of each tile, rows first
+
+template <int FMT, int EPI>
+struct Shape {
+  static constexpr int kWords = FMT == MOE_MXFP8 ? 1 : 2;  // scale words per row and K step
+  static constexpr int kTiles = EPI == MX_SWIGLU ? 2 : 1;  // weight tiles per item
+  static constexpr int kStageBytes = kTiles * W_BYTES + X_BYTES;
+  static constexpr int kStages = EPI == MX_SWIGLU ? 4 : 8;
+  static constexpr int kSfBytes = SF_WORDS * MX_SF_BYTES;  // per operand tile and buffer
+  static constexpr int kSfBuf = (kTiles + 1) * kSfBytes;   // the rows', then the weights'
+  static constexpr int kOffSf = kStages * kStageBytes;
+  static constexpr int kOffTail = kOffSf + 2 * kSfBuf;
+};
+
+struct __align__(8) SmemTail {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t sf_full[2];
+  uint64_t sf_empty[2];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  float tok_w[EPI_WARPS][CHUNK];  // MX_ROWS: each epilogue warp's copy of the chunk's
+  int tok_d[EPI_WARPS][CHUNK];    //   row weights and output rows
+  MxGroups groups;
+};
+
+template <int FMT>
+__device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (FMT == MOE_MXFP8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_copy_sf(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+
+// Scale words [w0, w0 + nw) of `rows` rows (`src` + lane + 32 j of each word, `pitch`
+// words from one word to the next) into a buffer: 16-byte row l of a word holds
+// those of rows l, l + 32, l + 64, l + 96.
+template <int J>
+__device__ __forceinline__ void load_words(uint32_t (&v)[SF_WORDS][4], const uint32_t* src,
+                                           size_t pitch, int nw, int rows, int lane) {
+#pragma unroll
+  for (int w = 0; w < SF_WORDS; ++w)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[w][j] = j < J && w < nw && lane + 32 * j < rows ? src[w * pitch + lane + 32 * j] : 0u;
+}
+
+__device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[SF_WORDS][4]) {
+#pragma unroll
+  for (int w = 0; w < SF_WORDS; ++w) st_shared_v4(addr + w * MX_SF_BYTES, v[w]);
+}
+
+template <int FMT, int EPI>
+__global__ void __launch_bounds__(THREADS, 1)
+    grouped_mx_few_kernel(const __grid_constant__ CUtensorMap tmW,
+                          const __grid_constant__ CUtensorMap tmX, const MxGemmArgs args) {
+  using S = Shape<FMT, EPI>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  SmemTail& st = *reinterpret_cast<SmemTail*>(smem + S::kOffTail);
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&st.full[s], 1);
+      mbar_init(&st.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&st.sf_full[b], 2);
+      mbar_init(&st.sf_empty[b], 1);
+      mbar_init(&st.tfull[b], 1);
+      mbar_init(&st.tempty[b], EPI_WARPS);
+    }
+    mbar_init(&st.drain, 1);
+    st.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(&st.tmem_base, TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();  // what comes before reads nothing that an earlier kernel writes
+  const int total = mx_group_table<CHUNK, THREADS>(args, st.groups) * args.n_tiles;
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = uniform(st.tmem_base);
+  const WaitCtx wc{&st.abort_flag, args.status, args.timeout_ns};
+  const int first = blockIdx.x, step = gridDim.x;
+  if (first < total) {
+    const int k_steps = (args.k_bytes + KB - 1) / KB;
+    const int* mts = st.groups.mt_start;
+    const int* rs = st.groups.row_start;
+    const int dm = step / args.n_tiles, dn = step - dm * args.n_tiles;
+    TileWalk<CHUNK> walk;
+    walk.start(first, args.n_tiles, args.groups, mts);
+    const uint32_t smem0 = smem_u32(smem), sf0 = smem0 + S::kOffSf;
+
+    if (warp == 0) {
+      // ------------------------------------------------ TMA producer
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      bool ok = true;
+      for (int item = first; ok && item < total; item += step) {
+        if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
+        const Tile t = walk.tile(mts, rs);
+        const int w_row = t.nt * WM;
+        const int nb = (t.rows + XBOX - 1) / XBOX;
+        const uint32_t tx = S::kTiles * W_BYTES + nb * XBOX * KB;
+        for (int ks = 0; ks < k_steps; ++ks) {
+          if (!__all_sync(FULL, mbar_wait(&st.empty[stage], phase ^ 1u, wc, 71))) {
+            ok = false;
+            break;
+          }
+          uint8_t* sx = smem + (size_t)stage * S::kStageBytes;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&st.full[stage], tx);
+#pragma unroll
+            for (int w = 0; w < S::kTiles; ++w)
+              tma_load_3d(sx + X_BYTES + w * W_BYTES, &tmW, &st.full[stage], ks * KB,
+                          w_row + w * args.b_second, t.g);
+            for (int b = 0; b < nb; ++b)
+              tma_load_2d(sx + b * XBOX * KB, &tmX, &st.full[stage], ks * KB, t.row0 + b * XBOX);
+          }
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == S::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        for (int s = 0; s < S::kStages; ++s)
+          if ((armed >> s) & 1u)
+            mbar_wait_drain(&st.full[s], (armed_parity >> s) & 1u, args.timeout_ns);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------ scales to TMEM and MMAs
+      constexpr int SF_STEPS = SF_WORDS / S::kWords;  // K steps per buffer of scales
+      int stage = 0, buf = 0, acc = 0;
+      uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
+      bool ok = true;
+      const uint64_t dx0 = sdesc_kmajor_sw128(smem0), dsf0 = sdesc_rows16(sf0);
+      const int last = args.k_bytes - (k_steps - 1) * KB;  // bytes of a row in the last step
+      for (int item = first; ok && item < total; item += step) {
+        if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
+        const Tile t = walk.tile(mts, rs);
+        const uint32_t idesc = idesc_mx<FMT>(WM, (t.rows + 15) & ~15);
+        const uint32_t d = tmem_base + acc * ACC_COLS;
+        int chunk_left = 0;
+        uint64_t dsf = dsf0;
+        for (int ks = 0; ks < k_steps; ++ks) {
+          if (chunk_left == 0) {
+            if (!__all_sync(FULL, mbar_wait(&st.sf_full[buf], sf_phase, wc, 72))) {
+              ok = false;
+              break;
+            }
+            chunk_left = SF_STEPS;
+            dsf = dsf0 + static_cast<uint64_t>(buf * (S::kSfBuf >> 4));
+          }
+          if (!__all_sync(FULL, mbar_wait(&st.full[stage], phase, wc, 73))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          --chunk_left;
+          const bool chunk_done = chunk_left == 0 || ks + 1 == k_steps;
+          const uint32_t sf = tmem_base + TMEM_SF + 32 * stage;
+          const uint64_t dx = dx0 + static_cast<uint64_t>(stage * (S::kStageBytes >> 4));
+          if (elect_one()) {
+#pragma unroll
+            for (int o = 0; o < S::kTiles + 1; ++o)
+#pragma unroll
+              for (int w = 0; w < S::kWords; ++w)
+                tmem_copy_sf(sf + 4 * (S::kWords * o + w),
+                             dsf + ((o * S::kSfBytes + w * MX_SF_BYTES) >> 4));
+          }
+          if (ks == 0) {
+            if (!__all_sync(FULL, mbar_wait(&st.tempty[acc], acc_phase ^ 1u, wc, 74))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+          }
+          if (elect_one()) {
+            // 32 bytes of every row per MMA; the scale word, and the byte in it
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (ks + 1 < k_steps || kk * 32 < last) {
+                const uint32_t word = 4 * (kk * S::kWords / 4);
+                const uint32_t id = idesc_sf(idesc, FMT == MOE_MXFP8 ? kk : 2 * (kk & 1));
+#pragma unroll
+                for (int w = 0; w < S::kTiles; ++w)
+                  umma_mx<FMT>(d + w * CHUNK, dx + ((X_BYTES + w * W_BYTES) >> 4) + 2 * kk,
+                               dx + 2 * kk, id, sf + 4 * S::kWords * (1 + w) + word, sf + word,
+                               (ks | kk) != 0 ? 1u : 0u);
+              }
+            umma_commit(&st.empty[stage]);
+            if (chunk_done) umma_commit(&st.sf_empty[buf]);
+            if (ks + 1 == k_steps) umma_commit(&st.tfull[acc]);
+          }
+          dsf += S::kWords * (MX_SF_BYTES >> 4);
+          if (chunk_done) {
+            chunk_left = 0;
+            buf ^= 1;
+            if (buf == 0) sf_phase ^= 1u;
+          }
+          if (++stage == S::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (elect_one()) {
+        umma_commit(&st.drain);  // all of this warp's MMAs are done
+        mbar_wait_drain(&st.drain, 0, args.timeout_ns);
+      }
+      __syncwarp();
+    } else if (warp < EPI_WARP0) {
+      // ------------------------------------------------ scales (warp 2: weight tile 0; 3: the rest)
+      int buf = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int item = first; ok && item < total; item += step) {
+        if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
+        const Tile t = walk.tile(mts, rs);
+        for (int w0 = 0; w0 < args.words; w0 += SF_WORDS) {
+          const int nw = min(SF_WORDS, args.words - w0);
+          const int n0 = t.nt * WM + (warp == 2 ? 0 : args.b_second);  // first weight row
+          const uint32_t* wsrc =
+              args.b_scales + ((size_t)t.g * args.words + w0) * args.n_rows + n0;
+          const uint32_t dst = sf0 + buf * S::kSfBuf + 16 * lane;
+          uint32_t v[SF_WORDS][4], x[SF_WORDS][4];
+          if (warp == 2 || S::kTiles == 2)
+            load_words<4>(v, wsrc, args.n_rows, nw, args.n_rows - n0, lane);
+          if (warp == 3)
+            load_words<2>(x, args.a_scales + (size_t)w0 * args.rows + t.row0, args.rows, nw, t.rows,
+                          lane);
+          if (!__all_sync(FULL, mbar_wait(&st.sf_empty[buf], phase ^ 1u, wc, 75))) {
+            ok = false;
+            break;
+          }
+          if (warp == 2 || S::kTiles == 2)
+            store_words(dst + (warp == 2 ? 1 : 2) * S::kSfBytes, v);
+          if (warp == 3) store_words(dst, x);
+          fence_proxy_async_smem();  // these writes -> tcgen05.cp
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&st.sf_full[buf]);
+          buf ^= 1;
+          if (buf == 0) phase ^= 1u;
+        }
+      }
+    } else {
+      // ------------------------------------------------ epilogue warps 4..7
+      const int q = warp & 3;
+      const int ew = warp - EPI_WARP0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      for (int item = first; item < total; item += step) {
+        if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
+        const Tile t = walk.tile(mts, rs);
+        const int col0 = t.nt * WM + q * 32;  // the warp's first output column
+        if constexpr (EPI == MX_ROWS) {
+#pragma unroll
+          for (int j = 0; j < CHUNK / 32; ++j) {
+            const int n = lane + 32 * j;
+            if (n < t.rows) {
+              const int row = t.row0 + n;
+              int dest = args.row_dest ? args.row_dest[row] : row;
+              if (dest < 0 || dest >= args.out_rows) dest = -1;
+              st.tok_d[ew][n] = dest;
+              st.tok_w[ew][n] = args.row_w ? args.row_w[row] : 1.0f;
+            }
+          }
+          __syncwarp();
+        }
+        if (!__all_sync(FULL, mbar_wait(&st.tfull[acc], acc_phase, wc, 76))) break;
+        tc_fence_after_sync();
+        const uint32_t tb =
+            tmem_base + acc * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
+        const bool col_ok = col0 < args.n_valid;  // whole blocks of 32 columns
+#pragma unroll 1
+        for (int n0 = 0; n0 < t.rows; n0 += 16) {
+          uint32_t g[16];
+          tmem_ld_32x32b_x16(tb + n0, g);
+          if constexpr (EPI == MX_ROWS) {
+            tmem_ld_wait();
+            if (col_ok) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int n = n0 + j;
+                if (n < t.rows && st.tok_d[ew][n] >= 0)
+                  static_cast<__nv_bfloat16*>(
+                      args.out)[(size_t)st.tok_d[ew][n] * args.n_valid + col0 + lane] =
+                      __float2bfloat16_rn(st.tok_w[ew][n] * __uint_as_float(g[j]));
+              }
+            }
+          } else {
+            uint32_t u[16];
+            tmem_ld_32x32b_x16(tb + CHUNK + n0, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int n = n0 + j;
+              if (n < t.rows) {
+                const int row = t.row0 + n;
+                uint32_t byte = 0;  // a word's bytes past the last column's block are 0
+                if (col_ok) {
+                  const float h = silu_f(__uint_as_float(g[j])) * __uint_as_float(u[j]);
+                  byte = mx_scale_byte<FMT>(
+                      __reduce_max_sync(FULL, __float_as_uint(h) & 0x7fffffffu));
+                  const float s = byte == 255u ? 0.0f : h * mx_inverse_scale(byte);
+                  uint8_t* out = static_cast<uint8_t*>(args.out) +
+                                 ((size_t)row * args.n_valid + col0) / MxFmt<FMT>::kPerByte;
+                  if constexpr (FMT == MOE_MXFP8) {
+                    out[lane] = static_cast<uint8_t>(mx_pack_e4m3(s, 0.f, 0.f, 0.f));
+                  } else {
+                    const float o = __shfl_xor_sync(FULL, s, 1);
+                    if ((lane & 1) == 0) out[lane >> 1] = mx_pack_e2m1_pair(s, o);
+                  }
+                }
+                if (lane == 0)
+                  reinterpret_cast<uint8_t*>(args.out_scales + (size_t)t.nt * args.rows + row)[q] =
+                      static_cast<uint8_t>(byte);
+              }
+            }
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st.tempty[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// Rows of codes in boxes of 128 bytes x box_rows; zeros past the ends.
+cudaError_t make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
+                           uint32_t box_rows) {
+  const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {KB, box_rows};
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t make_tmap_matrices(CUtensorMap* map, const void* base, uint64_t groups, uint64_t rows,
+                               uint64_t row_bytes) {
+  const cuuint64_t dims[3] = {row_bytes, rows, groups};
+  const cuuint64_t strides[2] = {row_bytes, rows * row_bytes};
+  const cuuint32_t box[3] = {KB, WM, 1};
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int FMT, int EPI>
+cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& args,
+                   int grid, cudaStream_t stream) {
+  constexpr size_t smem = 1024 + Shape<FMT, EPI>::kOffTail + sizeof(SmemTail);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static std::atomic<int> smem_set[MAX_DEVICES];
+  const cudaError_t e =
+      set_smem_limit_per_device(grouped_mx_few_kernel<FMT, EPI>, (int)smem, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_chained(grouped_mx_few_kernel<FMT, EPI>, dim3(grid), dim3(THREADS), smem, stream,
+                        tmW, tmX, args);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_mx_few(int fmt, int epi, const void* a, const void* b, MxGemmArgs args,
+                                  cudaStream_t stream) {
+  if (args.groups > MX_MAX_GROUPS) return cudaErrorInvalidValue;
+  CUtensorMap tmW, tmX;
+  cudaError_t e;
+  if ((e = make_tmap_matrices(&tmW, b, args.groups, args.n_rows, args.k_bytes)) != cudaSuccess)
+    return e;
+  if ((e = make_tmap_rows(&tmX, a, args.rows, args.k_bytes, XBOX)) != cudaSuccess) return e;
+  args.n_out_tile = WM;
+  args.n_tiles = (args.n_valid + WM - 1) / WM;
+  args.b_second = args.n_valid;  // MX_SWIGLU: the up rows
+  const long long items = ((long long)args.rows / CHUNK + args.groups) * args.n_tiles;
+  const int sms = num_sms();
+  const int grid = (int)(items < sms ? items : sms);
+  if (fmt == MOE_MXFP8)
+    return epi == MX_SWIGLU ? launch<MOE_MXFP8, MX_SWIGLU>(tmW, tmX, args, grid, stream)
+                            : launch<MOE_MXFP8, MX_ROWS>(tmW, tmX, args, grid, stream);
+  return epi == MX_SWIGLU ? launch<MOE_MXFP4, MX_SWIGLU>(tmW, tmX, args, grid, stream)
+                          : launch<MOE_MXFP4, MX_ROWS>(tmW, tmX, args, grid, stream);
+}
+
+}  // namespace rmoe

@@ -231,12 +231,15 @@ struct MxGemmArgs {
   int* status;
   int clear_status;          // 1: the status word is cleared first
   unsigned long long timeout_ns;
-  int n_tiles, n_out_tile, b_second;  // set by launch_grouped_mx
+  int n_tiles, n_out_tile, b_second;  // set by the launchers
 };
 
 // a: codes [rows, k_bytes]; b: codes [groups, n_rows, k_bytes].
 cudaError_t launch_grouped_mx(int fmt, int epi, const void* a, const void* b, MxGemmArgs args,
                               cudaStream_t stream);
+// The same for few rows per group (grouped_mx_few.cu).
+cudaError_t launch_grouped_mx_few(int fmt, int epi, const void* a, const void* b, MxGemmArgs args,
+                                  cudaStream_t stream);
 cudaError_t launch_gather_mx(const uint8_t* codes, const uint8_t* scales, const int* tok_of, int T,
                              int R, int row_bytes, int words, uint8_t* codes_out,
                              uint8_t* scales_out, cudaStream_t stream);

@@ -89,6 +89,17 @@ __device__ __forceinline__ uint32_t mx_pack_e2m1(const float* v) {
   return r;
 }
 
+// Two E2M1 codes in a byte (lo in the low nibble) of values within +-6.
+__device__ __forceinline__ uint8_t mx_pack_e2m1_pair(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0;\n\t.reg .b16 l;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "mov.b16 l, {b0, b0};\n\tcvt.u32.u16 %0, l;\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return static_cast<uint8_t>(r);
+}
+
 // Codes of N consecutive elements (N a multiple of 8) of one block whose scale
 // byte is given; out holds N / 4 (MXFP8) or N / 8 (MXFP4) words.
 template <int FMT, int N>

@@ -211,9 +211,10 @@ def test_add_rmsnorm_propagates_nan_to_its_row_alone():
 
 
 # ------------------------------------------------------------------ products
-SHAPES = [  # R, E, N, K
+SHAPES = [  # R, E, N, K; up to 64 rows an expert on average the operands are swapped
     (1, 1, 32, 32), (8, 16, 64, 96), (40, 3, 96, 160), (257, 5, 160, 352), (300, 2, 544, 512),
-    (600, 1, 256, 128), (1000, 7, 288, 1056), (515, 128, 64, 256),
+    (600, 1, 256, 128), (1000, 7, 288, 1056), (515, 128, 64, 256), (65, 1, 32, 32),
+    (130, 2, 128, 2112), (128, 2, 128, 2112), (64, 1, 416, 1184), (200, 4, 64, 64),
 ]
 
 
