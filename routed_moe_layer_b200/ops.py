@@ -577,18 +577,29 @@ def _ws_bytes(name: str, *sizes: int) -> int:
     return max(int(getattr(lib(), name)(*sizes)), 256)
 
 
-def _need_mx(codes: torch.Tensor, scales: torch.Tensor, name: str, lead: Sequence[int], rows: int,
+def _need_mx(codes: torch.Tensor, scales: torch.Tensor, name: str, lead: tuple, rows: int,
              K: int, fmt: int):
-    _is(codes, f"{name}_codes", torch.uint8, (*lead, rows, K if fmt == 1 else K // 2))
-    _is(scales, f"{name}_scales", torch.uint8, (*lead, mx_words(K), rows, 4))
+    u8 = torch.uint8
+    want_c = lead + (rows, K if fmt == 1 else K // 2)
+    want_s = lead + ((K + 127) // 128, rows, 4)
+    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and codes.is_cuda
+            and codes.dtype is u8 and scales.dtype is u8 and codes.shape == want_c
+            and scales.shape == want_s and codes.is_contiguous() and scales.is_contiguous()
+            and scales.device == codes.device):
+        _need(codes, f"{name}_codes", u8, want_c)
+        _need(scales, f"{name}_scales", u8, want_s)
+        _one_device(codes, scales)
 
 
 def _matrices(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dim() not in (2, 3):
+    shape = tuple(t.shape)
+    if len(shape) == 3:
+        return shape[0], shape[:1], shape[1], shape[2]
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a matrix or a stack of matrices")
-    return (t.shape[0] if t.dim() == 3 else 1), tuple(t.shape[:-2]), t.shape[-2], t.shape[-1]
+    return 1, (), shape[0], shape[1]
 
 
 def mx_quantize(x: torch.Tensor, fmt: str):
@@ -610,7 +621,7 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: str) -> torch.
     G, lead, rows, K = _matrices(codes, "codes")
     K = K if f == 1 else 2 * K
     _need_mx(codes, scales, "x", lead, rows, K, f)
-    dev = _one_device(codes, scales)
+    dev = codes.device
     x = codes.new_empty((*lead, rows, K), dtype=torch.bfloat16)
     _call("moe_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), G, rows, K, f,
           x.data_ptr())
@@ -712,7 +723,7 @@ def grouped_mm_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.
     _need_mx(w_codes, w_scales, "w", (E,), N, K, f)
     _is(offsets, "offsets", torch.int32, (E + 1,))
     y = _mx_out(R, N, x_codes.device, row_w, row_dest, out, out_rows)
-    dev = _one_device(x_codes, x_scales, w_codes, w_scales, offsets, row_w, row_dest, y, workspace)
+    dev = _one_device(x_codes, w_codes, offsets, row_w, row_dest, y, workspace)
     if workspace is None:
         workspace = y.new_empty(256, dtype=torch.uint8)
     _call("moe_grouped_mm_mx", dev, x_codes.data_ptr(), x_scales.data_ptr(), offsets.data_ptr(), R,
@@ -746,8 +757,7 @@ def expert_rows_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, offsets: torch
         R = tok_of.numel()
         _is(tok_of, "tok_of", torch.int32, (R,))
     y = _mx_out(R, H, x_codes.device, row_w, row_dest, y, y_rows)
-    dev = _one_device(x_codes, x_scales, offsets, w13_codes, w13_scales, w2_codes, w2_scales,
-                      row_dest, row_w, tok_of, y, workspace)
+    dev = _one_device(x_codes, offsets, w13_codes, w2_codes, row_dest, row_w, tok_of, y, workspace)
     if workspace is None:
         workspace = y.new_empty(_ws_bytes("moe_expert_rows_mx_workspace_bytes", R, H, E, I, f,
                                           int(tok_of is not None)), dtype=torch.uint8)
