@@ -768,6 +768,25 @@ def expert_rows_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, offsets: torch
     return y
 
 
+def forward_mx(x: torch.Tensor, Wr: torch.Tensor, bias: torch.Tensor, w13: tuple, w2: tuple,
+               ws13: Optional[torch.Tensor], ws2: Optional[torch.Tensor], cfg: BlockConfig,
+               fmt: str, x_mx: Optional[tuple] = None, residual: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None,
+               token_mask: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Block forward with routed experts on MX operands: the steps of moe_forward
+    as calls of the entry points (route, permute, expert_rows_mx, dense_ffn for
+    the bf16 shared expert, combine_rows); returns out bf16 [T,H].
+    w13, w2: (codes, scales) of [E,2I,H] and [E,H,I]; x_mx: (codes, scales) of x
+    where add_rmsnorm has made them, else x is quantised here."""
+    ids, w = route(x, Wr, bias, cfg, token_mask=token_mask)
+    p = permute(ids, cfg, topk_w=w)
+    codes, scales = mx_quantize(x, fmt) if x_mx is None else x_mx
+    y = expert_rows_mx(codes, scales, p["expert_offsets"], *w13, *w2, None, fmt, row_w=p["w_of"],
+                       tok_of=p["tok_of"])
+    shared = dense_ffn(x, ws13, ws2) if cfg.I_shared > 0 else None
+    return combine_rows(y, p["row_of"], cfg.top_k, shared=shared, residual=residual, out=out)
+
+
 def read_device_status(workspace: torch.Tensor):
     """Synchronises the current stream; returns (code, site) and clears the word."""
     site = ctypes.c_int32(0)

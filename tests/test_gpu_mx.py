@@ -11,8 +11,10 @@ import pytest
 import torch
 
 from oracle import bf16_round, mx_oracle as mx
-from routed_moe_layer_b200 import ops
+from routed_moe_layer_b200 import inputs, ops
+from routed_moe_layer_b200.ops import BlockConfig
 from tests.parity import to_np
+from tests.test_zz_write_guards import guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -409,3 +411,143 @@ def test_expert_rows_mx_token_outside_counts_as_zeros():
     tok = torch.tensor([0, -1, 4, 3], dtype=torch.int32, device=DEV)
     y = ops.expert_rows_mx(xc, xs, off, w13c, w13s, w2c, w2s, None, "mxfp8", tok_of=tok)
     assert (y[1:3] == 0).all() and (y[0] != 0).any() and (y[3] != 0).any()
+
+
+# ------------------------------------------------------------------ together
+def block(T, H, E, I, Is, k, seed):
+    cfg = BlockConfig(T=T, H=H, E=E, I=I, I_shared=Is, top_k=k, n_group=4, topk_group=2)
+    d = inputs.make_block_inputs(T, H, seed=seed, E=E, I=I, I_shared=Is, unit_scale=True)
+    return cfg, {n: (None if v is None else v.to(DEV)) for n, v in d.items()}
+
+
+def run_layer(d, cfg, w13, w2, stream_in, gamma, fmt):
+    """One layer of a stack: norm of the stream with the last block's output, the block."""
+    s, xn, c, sc = ops.add_rmsnorm(d["x"], stream_in, gamma, fmt=fmt)
+    return s, xn, c, sc, ops.forward_mx(xn, d["Wr"], d["bias"], w13, w2, d["ws13"], d["ws2"], cfg,
+                                        fmt, x_mx=(c, sc), residual=s)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [1, 50, 700])
+def test_norm_router_experts_restore_together(T, fmt):
+    H, E, I, k = 256, 16, 96, 4
+    cfg, d = block(T, H, E, 128, 0, k, T)  # its bf16 experts are not used
+    w13c, w13s, w13 = operands(2 * I, H, fmt, 7, lead=E, scale=H ** -0.5)
+    w2c, w2s, w2 = operands(H, I, fmt, 8, lead=E, scale=I ** -0.5)
+    res = inputs.make_tokens(T, H, seed=3).to(DEV)
+    gamma = (1 + 0.1 * torch.randn(H, generator=gen(4))).to(DEV)
+    s, xn, c, sc, out = run_layer(d, cfg, (w13c, w13s), (w2c, w2s), res, gamma, fmt)
+    ids, w = ops.route(xn, d["Wr"], d["bias"], cfg)
+    # the oracle under the GPU's routing, from the GPU's narrow tokens (tested bit for bit above)
+    x = mx.mx_values(*mx.mx_load(c.cpu().numpy(), sc.cpu().numpy(), H, fmt), fmt)
+    flat = ids.cpu().reshape(-1).long()
+    order = torch.argsort(flat, stable=True)
+    off = np.concatenate([[0], np.cumsum(np.bincount(flat.numpy(), minlength=E))])
+    rw = w.cpu().reshape(-1)[order].numpy().astype(np.float64)
+    y, tol = experts_tolerance(x[(order // k).numpy()], w13, w2, off, fmt, rw)
+    ref, bound = to_np(s).astype(np.float64), np.zeros((T, H))
+    for row, slot in enumerate(order.tolist()):
+        ref[slot // k] += y[row]
+        bound[slot // k] += tol[row]
+    # the restore: k + 1 terms added in fp32 (half a step of the partial sums each), one rounding
+    mag = np.abs(to_np(s)) + sum(np.abs(y[np.argsort(order.numpy())][j::k]) for j in range(k))
+    bound += (k + 1) * 2.0 ** -24 * (mag + bound)
+    bound += 2.0 ** -8 * (np.abs(ref) + bound)
+    assert np.all(np.abs(to_np(out) - ref) <= bound * (1 + 1e-6))
+
+
+@pytest.mark.parametrize("Is", [0, 96 * 2])
+def test_forward_mx_is_its_steps(Is):
+    T, H, E, I, k = 300, 256, 16, 128, 4
+    cfg, d = block(T, H, E, I, Is, k, 5)
+    w13, w2 = ops.mx_quantize(d["w13"], "mxfp8"), ops.mx_quantize(d["w2"], "mxfp8")
+    mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+    mask[250:] = 0
+    out = ops.forward_mx(d["x"], d["Wr"], d["bias"], w13, w2, d["ws13"], d["ws2"], cfg, "mxfp8",
+                         token_mask=mask)
+    full = ops.forward_mx(d["x"], d["Wr"], d["bias"], w13, w2, d["ws13"], d["ws2"], cfg, "mxfp8")
+    assert torch.equal(out[:250], full[:250])  # real tokens: the bits of the call without padding
+    shared = ops.dense_ffn(d["x"], d["ws13"], d["ws2"]) if Is else torch.zeros_like(d["x"])
+    assert torch.equal(out[250:], shared[250:])
+    # near the bf16 block: what eight bits change is a few percent of the output
+    ref = ops.forward(d["x"], d["Wr"], d["bias"], d["w13"], d["w2"], d["ws13"], d["ws2"], cfg)
+    assert (full - ref).float().norm() < 0.2 * ref.float().norm()
+
+
+def test_captured_replayed_and_on_two_streams():
+    T, H, E, I, k = 96, 512, 16, 128, 4
+    cfg, d = block(T, H, E, I, 0, k, 6)
+    w13, w2 = ops.mx_quantize(d["w13"], "mxfp4"), ops.mx_quantize(d["w2"], "mxfp4")
+    res = inputs.make_tokens(T, H, seed=3).to(DEV)
+    gamma = torch.ones(H, device=DEV)
+    want = [t.clone() for t in run_layer(d, cfg, w13, w2, res, gamma, "mxfp4")]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    for _ in range(2):  # two graphs of the same leaves, each with its own workspaces
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(run_layer(d, cfg, w13, w2, res, gamma, "mxfp4"))
+        graphs.append(g)
+    keep = d["x"].clone()
+    for _ in range(3):
+        d["x"].copy_(res)  # other inputs, then the first ones again: nothing is kept
+        graphs[0].replay()
+        assert not torch.equal(outs[0][4], want[4])
+        d["x"].copy_(keep)
+        for g, o in zip(graphs, outs):
+            g.replay()
+            for a, b in zip(o, want):
+                assert torch.equal(a, b)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):  # overlapping calls
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(run_layer(d, cfg, w13, w2, res, gamma, "mxfp4"))
+    torch.cuda.synchronize()
+    for o in got:
+        for a, b in zip(o, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R", [60, 900])  # swapped operands, pair tiles
+def test_products_write_only_their_rows_and_leave_inputs(R, fmt):
+    E, N, K = 4, 96, 160
+    xc, xs, _ = operands(R, K, fmt, 1)
+    wc, wsc, _ = operands(N, K, fmt, 2, lead=E)
+    off = torch.from_numpy(groups(R, E, 3)).to(DEV)
+    before = [t.clone() for t in (xc, xs, wc, wsc, off)]
+    y, c_y = guarded((R, N), torch.bfloat16, DEV)
+    ws, c_ws = guarded((256,), torch.uint8, DEV)
+    ops.grouped_mm_mx(xc, xs, wc, wsc, off, fmt, out=y, workspace=ws)
+    c, s = operands(2 * N, K, fmt, 5, lead=E)[:2]
+    w2c, w2s = operands(K, N, fmt, 6, lead=E)[:2]
+    z, c_z = guarded((R, K), torch.bfloat16, DEV)
+    n = ops.lib().moe_expert_rows_mx_workspace_bytes(R, K, E, N, ops.MX_FORMATS[fmt], 1)
+    ws2, c_ws2 = guarded((n,), torch.uint8, DEV)
+    tok = torch.arange(R, dtype=torch.int32, device=DEV).flip(0).contiguous()
+    ops.expert_rows_mx(xc, xs, off, c, s, w2c, w2s, None, fmt, tok_of=tok, y=z, workspace=ws2)
+    assert ops.read_device_status(ws2)[0] == 0
+    for check in (c_y, c_ws, c_z, c_ws2):
+        check()
+    for a, b in zip((xc, xs, wc, wsc, off), before):
+        assert torch.equal(a, b)
+
+
+def test_products_with_outputs_past_32_bits():
+    R, N, K = 140000, 16384, 32  # 2.29e9 outputs
+    g = gen(1)
+    x = torch.randn(R, K, generator=g).bfloat16().to(DEV)
+    w = torch.randn(1, N, K, generator=g).bfloat16().to(DEV)
+    off = torch.tensor([0, R], dtype=torch.int32, device=DEV)
+    y = ops.grouped_mm(x, w, off)
+    last = torch.tensor([0, 5], dtype=torch.int32, device=DEV)
+    assert torch.equal(y[-5:], ops.grouped_mm(x[-5:].contiguous(), w, last))
+    for fmt in FMTS:
+        xc, xs = ops.mx_quantize(x, fmt)
+        wc, wsc = ops.mx_quantize(w, fmt)
+        ops.grouped_mm_mx(xc, xs, wc, wsc, off, fmt, out=y)
+        tail = ops.grouped_mm_mx(xc[-5:].contiguous(), xs[:, -5:].contiguous(), wc, wsc, last, fmt)
+        assert torch.equal(y[-5:], tail)
