@@ -62,8 +62,6 @@ struct __align__(8) SmemTail {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  float tok_w[EPI_WARPS][CHUNK];  // MX_ROWS: each epilogue warp's copy of the chunk's
-  int tok_d[EPI_WARPS][CHUNK];    //   row weights and output rows
   MxGroups groups;
 };
 
@@ -321,77 +319,87 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
       // ------------------------------------------------ epilogue warps 4..7
       const int q = warp & 3;
-      const int ew = warp - EPI_WARP0;
       int acc = 0;
       uint32_t acc_phase = 0;
       for (int item = first; item < total; item += step) {
         if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
         const Tile t = walk.tile(mts, rs);
         const int col0 = t.nt * WM + q * 32;  // the warp's first output column
+        // MX_ROWS: lane l holds output row (-1: none) and weight of rows l, l + 32
+        int dest[CHUNK / 32];
+        float w[CHUNK / 32];
         if constexpr (EPI == MX_ROWS) {
 #pragma unroll
           for (int j = 0; j < CHUNK / 32; ++j) {
-            const int n = lane + 32 * j;
-            if (n < t.rows) {
-              const int row = t.row0 + n;
-              int dest = args.row_dest ? args.row_dest[row] : row;
-              if (dest < 0 || dest >= args.out_rows) dest = -1;
-              st.tok_d[ew][n] = dest;
-              st.tok_w[ew][n] = args.row_w ? args.row_w[row] : 1.0f;
+            const int n = lane + 32 * j, row = t.row0 + n;
+            dest[j] = -1;
+            w[j] = 1.0f;
+            if (n < t.rows && col0 < args.n_valid) {
+              dest[j] = args.row_dest ? args.row_dest[row] : row;
+              if (dest[j] >= args.out_rows) dest[j] = -1;
+              if (args.row_w) w[j] = args.row_w[row];
             }
           }
-          __syncwarp();
         }
         if (!__all_sync(FULL, mbar_wait(&st.tfull[acc], acc_phase, wc, 76))) break;
         tc_fence_after_sync();
         const uint32_t tb =
             tmem_base + acc * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
-        const bool col_ok = col0 < args.n_valid;  // whole blocks of 32 columns
+        // 16 rows at a time, without branches between them: their shuffles,
+        // reductions and stores overlap (row by row they cost 170 cycles each,
+        // and bounded the call from 8 rows a group on)
 #pragma unroll 1
         for (int n0 = 0; n0 < t.rows; n0 += 16) {
           uint32_t g[16];
           tmem_ld_32x32b_x16(tb + n0, g);
           if constexpr (EPI == MX_ROWS) {
             tmem_ld_wait();
-            if (col_ok) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(args.out) + col0 + lane;
+            const int dl = n0 < 32 ? dest[0] : dest[1];
+            const float wl = n0 < 32 ? w[0] : w[1];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int n = n0 + j;
-                if (n < t.rows && st.tok_d[ew][n] >= 0)
-                  static_cast<__nv_bfloat16*>(
-                      args.out)[(size_t)st.tok_d[ew][n] * args.n_valid + col0 + lane] =
-                      __float2bfloat16_rn(st.tok_w[ew][n] * __uint_as_float(g[j]));
-              }
+            for (int j = 0; j < 16; ++j) {
+              const int d = __shfl_sync(FULL, dl, (n0 & 16) + j);
+              const float wj = __shfl_sync(FULL, wl, (n0 & 16) + j);
+              const __nv_bfloat16 v = __float2bfloat16_rn(wj * __uint_as_float(g[j]));
+              if (d >= 0) out[(size_t)d * args.n_valid] = v;
             }
           } else {
             uint32_t u[16];
             tmem_ld_32x32b_x16(tb + CHUNK + n0, u);
             tmem_ld_wait();
+            const int left = col0 < args.n_valid ? t.rows - n0 : 0;  // whole blocks of 32 columns
+            const int row = t.row0 + n0;
+            uint32_t bytes = 0;  // lane j: scale byte of row j
+            float h[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              h[j] = silu_f(__uint_as_float(g[j])) * __uint_as_float(u[j]);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int n = n0 + j;
-              if (n < t.rows) {
-                const int row = t.row0 + n;
-                uint32_t byte = 0;  // a word's bytes past the last column's block are 0
-                if (col_ok) {
-                  const float h = silu_f(__uint_as_float(g[j])) * __uint_as_float(u[j]);
-                  byte = mx_scale_byte<FMT>(
-                      __reduce_max_sync(FULL, __float_as_uint(h) & 0x7fffffffu));
-                  const float s = byte == 255u ? 0.0f : h * mx_inverse_scale(byte);
-                  uint8_t* out = static_cast<uint8_t*>(args.out) +
-                                 ((size_t)row * args.n_valid + col0) / MxFmt<FMT>::kPerByte;
-                  if constexpr (FMT == MOE_MXFP8) {
-                    out[lane] = static_cast<uint8_t>(mx_pack_e4m3(s, 0.f, 0.f, 0.f));
-                  } else {
-                    const float o = __shfl_xor_sync(FULL, s, 1);
-                    if ((lane & 1) == 0) out[lane >> 1] = mx_pack_e2m1_pair(s, o);
-                  }
-                }
-                if (lane == 0)
-                  reinterpret_cast<uint8_t*>(args.out_scales + (size_t)t.nt * args.rows + row)[q] =
-                      static_cast<uint8_t>(byte);
+              const uint32_t byte = mx_scale_byte<FMT>(
+                  __reduce_max_sync(FULL, __float_as_uint(h[j]) & 0x7fffffffu));
+              if (lane == j) bytes = byte;
+              h[j] = byte == 255u ? 0.0f : h[j] * mx_inverse_scale(byte);
+            }
+            uint8_t* out = static_cast<uint8_t*>(args.out) +
+                           ((size_t)row * args.n_valid + col0) / MxFmt<FMT>::kPerByte;
+            const int pitch = args.n_valid / MxFmt<FMT>::kPerByte;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if constexpr (FMT == MOE_MXFP8) {
+                const uint8_t c = static_cast<uint8_t>(mx_pack_e4m3(h[j], 0.f, 0.f, 0.f));
+                if (j < left) out[(size_t)j * pitch + lane] = c;
+              } else {
+                const float o = __shfl_xor_sync(FULL, h[j], 1);
+                const uint8_t c = mx_pack_e2m1_pair(h[j], o);
+                if (j < left && (lane & 1) == 0) out[(size_t)j * pitch + (lane >> 1)] = c;
               }
             }
+            // a word's bytes past the last column's block are 0
+            if (lane < t.rows - n0 && lane < 16)
+              reinterpret_cast<uint8_t*>(args.out_scales + (size_t)t.nt * args.rows + row + lane)[q] =
+                  static_cast<uint8_t>(left > 0 ? bytes : 0u);
           }
         }
         tc_fence_before_sync();
