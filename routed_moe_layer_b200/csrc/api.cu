@@ -691,13 +691,16 @@ MxGemmArgs mx_args(const uint8_t* a_scales, const int32_t* offsets, int32_t R, i
   return g;
 }
 
-// Few rows per group on average: the operands swapped.  128 groups of K = 1024,
-// N = 1024, swapped against pair tiles: MXFP8 8 rows 27.3 / 34.0 us, 16 rows
-// 29.0 / 34.7, 32 rows 36.5 / 35.5; MXFP4 (whose weights stream in half the time)
-// 8 rows 19.4 / 23.5, 16 rows 22.7 / 24.1, 32 rows (32 groups) 12.3 / 10.7.
+// Few rows per group on average: the operands swapped.  128 experts, H = 2048,
+// I = 768, cold L2, swapped against pair tiles.  Up (its output is one byte or
+// less a column): MXFP8 15 rows a group 88.2 / 92.4 us, 64 rows 94.9 / 94.0; MXFP4
+// 49.2 / 53.3, 52.5 / 55.6.  Rows of bf16, whose stores cost the swapped form's
+// four epilogue warps more: MXFP8 15 rows 54.4 / 59.7, 24 rows 59.0 / 61.1, 32 rows
+// 66.6 / 60.8; MXFP4 (whose weights stream in half the time) 15 rows 41.3 / 43.9,
+// 24 rows 48.4 / 44.5.
 cudaError_t mx_product(int fmt, int epi, const void* a, const void* b, const MxGemmArgs& g,
                        cudaStream_t s) {
-  const int64_t few = fmt == MOE_MXFP8 ? 24 : 16;
+  const int64_t few = epi == MX_SWIGLU ? 64 : fmt == MOE_MXFP8 ? 24 : 16;
   return g.rows <= few * g.groups ? launch_grouped_mx_few(fmt, epi, a, b, g, s)
                                   : launch_grouped_mx(fmt, epi, a, b, g, s);
 }
