@@ -319,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmSB);
   }
-  const int total = mx_group_table<TILE_M, THREADS>(args, st.groups) * args.n_tiles;
+  const int total = mx_group_table<TILE_M>(args, st.groups) * args.n_tiles;
   if (cluster >= total) return;  // the same for both CTAs of the cluster; nothing allocated yet
   cluster_sync();                // both CTAs' barriers exist before any cross-CTA traffic
 

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish();
   }
   pdl_wait();  // what comes before reads nothing that an earlier kernel writes
-  const int total = mx_group_table<CHUNK, THREADS>(args, st.groups) * args.n_tiles;
+  const int total = mx_group_table<CHUNK>(args, st.groups) * args.n_tiles;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();

@@ -35,8 +35,7 @@ struct Tile {
 };
 
 // The tiles (of TILE rows) of one CTA or cluster in order: every n-th, columns
-// fastest.  The warp finds the next one's group together (32 groups a look), since a search
-// by one thread, seven dependent loads, cost each role 1,300 cycles a tile.
+// fastest.  The warp finds the next one's group together (32 groups a look).
 template <int TILE>
 struct TileWalk {
   int g, mt, nt;
@@ -79,42 +78,65 @@ struct TileWalk {
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 // Rows of groups and the prefix of their tiles, from the caller's offsets.
-// Offsets that run backwards or past the rows are cut to the rows, so that no
-// access leaves the operands, and reported.
+// Offsets outside the rows are cut to them and ones that run backwards raised to
+// the largest before them, so that no access leaves the operands; both are
+// reported.
 struct MxGroups {
-  int bad_offsets;
   int mt_start[MX_MAX_GROUPS + 1];
   int row_start[MX_MAX_GROUPS + 1];
 };
 
 // All threads of the block; returns the number of row tiles.
-template <int TILE, int THREADS>
+template <int TILE>
 __device__ __forceinline__ int mx_group_table(const MxGemmArgs& a, MxGroups& t) {
-  if (threadIdx.x == 0) {
-    t.bad_offsets = 0;
-    if (blockIdx.x == 0 && a.clear_status) {
+  if (threadIdx.x < 32) {  // 5 offsets per lane
+    constexpr int PER = MX_MAX_GROUPS / 32 + 1;
+    const int lane = threadIdx.x;
+    if (lane == 0 && blockIdx.x == 0 && a.clear_status) {
       a.status[0] = 0;
       a.status[1] = 0;
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i <= a.groups; i += THREADS) {
-    const int o = a.offsets[i];
-    t.row_start[i] = min(max(o, 0), a.rows);
-    if (o < 0 || o > a.rows || (i > 0 && o < a.offsets[i - 1])) t.bad_offsets = 1;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0 && blockIdx.x == 0 && t.bad_offsets)
-    report_error(a.status, MOE_ERR_DEVICE_INDEX, 60);
-  if (threadIdx.x < 32) {  // exclusive prefix of tiles over groups (4 groups per lane)
-    constexpr int PER = MX_MAX_GROUPS / 32;
-    const int lane = threadIdx.x;
-    int loc[PER], sum = 0;
+    int at[PER];
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int g = lane * PER + q;
-      loc[q] = g < a.groups ? (max(t.row_start[g + 1] - t.row_start[g], 0) + TILE - 1) / TILE : 0;
+      at[q] = a.offsets[min(g, a.groups)];
+    }
+    int prev = __shfl_up_sync(FULL, at[PER - 1], 1);  // the offset before this lane's
+    if (lane == 0) prev = 0;
+    bool bad = false;
+    int low = prev;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      bad |= at[q] < low || at[q] > a.rows;
+      low = at[q];
+    }
+    if (__any_sync(FULL, bad)) {
+      if (lane == 0 && blockIdx.x == 0) report_error(a.status, MOE_ERR_DEVICE_INDEX, 60);
+      int top = 0;
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        top = max(top, min(at[q], a.rows));
+        at[q] = top;
+      }
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(FULL, top, off);
+        if (lane >= off) top = max(top, u);
+      }
+      prev = __shfl_up_sync(FULL, top, 1);
+      if (lane == 0) prev = 0;
+#pragma unroll
+      for (int q = 0; q < PER; ++q) at[q] = max(at[q], prev);
+    }
+    int loc[PER], sum = 0;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {  // loc: tiles of group g - 1
+      const int g = lane * PER + q;
+      if (g <= a.groups) t.row_start[g] = at[q];
+      loc[q] = g > 0 && g <= a.groups ? (at[q] - prev + TILE - 1) / TILE : 0;
       sum += loc[q];
+      prev = at[q];
     }
     int incl = sum;
 #pragma unroll
@@ -126,10 +148,9 @@ __device__ __forceinline__ int mx_group_table(const MxGemmArgs& a, MxGroups& t) 
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int g = lane * PER + q;
-      if (g < a.groups) t.mt_start[g] = run;
       run += loc[q];
+      if (g <= a.groups) t.mt_start[g] = run;
     }
-    if (lane == 31) t.mt_start[a.groups] = incl;
   }
   __syncthreads();
   return t.mt_start[a.groups];

@@ -158,12 +158,12 @@ __global__ void __launch_bounds__(256)
 // codes, scales = MX(xn).  TPR threads hold a row, V vectors of 8 elements
 // each (vector j*TPR + t, so that loads are whole lines), from the first load
 // to the last store: every tensor is read once.  fp32 sum of squares in a fixed
-// order (a thread's vectors, lanes by halving, warps in order).
-// FMT 0: no codes.
+// order (a thread's vectors, lanes by halving, warps in order).  sum may be x or
+// residual: a thread writes what it alone has read.  FMT 0: no codes.
 template <int FMT, int TPR, int V>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
-    add_rmsnorm_kernel(const uint4* __restrict__ x, const uint4* __restrict__ residual,
-                       const float4* __restrict__ gamma, float eps, int T, int H, uint4* sum,
+    add_rmsnorm_kernel(const uint4* x, const uint4* residual, const float4* __restrict__ gamma,
+                       float eps, int T, int H, uint4* sum,
                        uint4* __restrict__ xn, uint8_t* __restrict__ codes,
                        uint32_t* __restrict__ scales) {
   constexpr int BLOCK = TPR < 256 ? 256 : TPR;

@@ -628,6 +628,14 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: str) -> torch.
     return x
 
 
+def mx_block_scales(block_scales: torch.Tensor, rows: int) -> torch.Tensor:
+    """MX scales of a matrix or stack whose E4M3 codes have one UE8M0 byte per
+    128 x 128 block (the weights of forward_fp8): uint8 [..., ceil(rows/128), K/128]
+    -> [..., K/128, rows, 4].  The codes serve as "mxfp8" codes as they are."""
+    s = block_scales.transpose(-1, -2).repeat_interleave(128, dim=-1)[..., :rows]
+    return s.unsqueeze(-1).expand(*s.shape, 4).contiguous()
+
+
 def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
                 gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
                 fmt: Optional[str] = None, sum_out: Optional[torch.Tensor] = None):

@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import bf16_round, mx_oracle as mx
+from oracle import bf16_round, fp8_block_dequant, mx_oracle as mx
 from routed_moe_layer_b200 import inputs, ops
 from routed_moe_layer_b200.ops import BlockConfig
 from tests.parity import to_np
@@ -152,8 +152,22 @@ def test_quantize_offsets_past_32_bits():
 
 
 def test_empty_and_misaligned_calls():
-    c, s = ops.mx_quantize(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV), "mxfp4")
+    none = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
+    c, s = ops.mx_quantize(none, "mxfp4")
     assert c.shape == (0, 32) and s.shape == (1, 0, 4)
+    assert ops.mx_dequantize(c, s, "mxfp4").shape == (0, 64)
+    assert [t.shape[0] for t in ops.add_rmsnorm(none, none, fmt="mxfp8")] == [0, 0, 0, 1]
+    w = torch.ones(2, 32, 64, dtype=torch.bfloat16, device=DEV)
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    assert ops.grouped_mm(none, w, off).shape == (0, 32)
+    wc, ws = ops.mx_quantize(w, "mxfp4")
+    assert ops.grouped_mm_mx(c, s, wc, ws, off, "mxfp4").shape == (0, 32)
+    # rows, but none of them in a group
+    y = torch.full((5, 32), 7.0, dtype=torch.bfloat16, device=DEV)
+    x = torch.ones(5, 64, dtype=torch.bfloat16, device=DEV)
+    ops.grouped_mm(x, w, off, out=y)
+    ops.grouped_mm_mx(*ops.mx_quantize(x, "mxfp4"), wc, ws, off, "mxfp4", out=y)
+    assert (y == 7).all()
     buf = torch.zeros(4 * 64 + 8, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(RuntimeError, match="INVALID_ARG"):
         ops.mx_quantize(buf[4:4 + 256].view(4, 64), "mxfp8")  # 8 bytes off
@@ -311,6 +325,19 @@ def test_nan_blocks_reach_their_rows_and_columns_alone(fmt):
     nan[150] = False
     nan[:, 17] = False
     assert not nan.any()
+
+
+def test_block_scaled_fp8_weights_are_mx_weights():
+    """The weights of forward_fp8 (one scale per 128 x 128 block), their scales spread."""
+    E, N, K, R = 3, 320, 384, 150
+    w = inputs.make_fp8_weights(K, seed=1, E=E, I=N // 2, I_shared=0)
+    codes, blocks = w["w13_q"], w["w13_s"]
+    assert codes.shape == (E, N, K)
+    xc, xs, x = operands(R, K, "mxfp8", 2)
+    off = groups(R, E, 3)
+    y = ops.grouped_mm_mx(xc, xs, codes.to(DEV), ops.mx_block_scales(blocks.to(DEV), N),
+                          torch.from_numpy(off).to(DEV), "mxfp8")
+    check_product(y, x, fp8_block_dequant(codes.numpy(), blocks.numpy()), off)
 
 
 def test_bad_offsets_are_reported_and_write_nothing_outside():
