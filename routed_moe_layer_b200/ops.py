@@ -537,27 +537,27 @@ def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _is(t, name: str, dtype, shape: Sequence[int]):
-    """_need for the calls whose host time counts: one test when all is well."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous()):
+def _is(t, name: str, dtype, shape: Sequence[int], dev: int):
+    """_need, and that t is on device ``dev``: one test when all is well, for the
+    calls whose host time counts."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and dev >= 0 and t.is_contiguous()):
         _need(t, name, dtype, shape)
+        raise ValueError(f"all tensors must be on cuda:{dev}, {name} is on {t.device}")
 
 
-def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
-    return dev
+def _device(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    return t.get_device()
 
 
-def _call(name: str, dev: torch.device, *args):
-    """Calls entry point ``name`` with dev current, on dev's current stream."""
+def _call(name: str, dev: int, *args):
+    """Calls entry point ``name`` with device ``dev`` current, on its current stream."""
     fn = getattr(_lib or lib(), name)
     # what torch.cuda.current_stream(dev).cuda_stream reads, without the Stream object
-    stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    if dev.index == torch._C._cuda_getDevice():
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
         code = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -578,17 +578,16 @@ def _ws_bytes(name: str, *sizes: int) -> int:
 
 
 def _need_mx(codes: torch.Tensor, scales: torch.Tensor, name: str, lead: tuple, rows: int,
-             K: int, fmt: int):
+             K: int, fmt: int, dev: int):
     u8 = torch.uint8
     want_c = lead + (rows, K if fmt == 1 else K // 2)
     want_s = lead + ((K + 127) // 128, rows, 4)
-    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and codes.is_cuda
+    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor)
             and codes.dtype is u8 and scales.dtype is u8 and codes.shape == want_c
-            and scales.shape == want_s and codes.is_contiguous() and scales.is_contiguous()
-            and scales.device == codes.device):
-        _need(codes, f"{name}_codes", u8, want_c)
-        _need(scales, f"{name}_scales", u8, want_s)
-        _one_device(codes, scales)
+            and scales.shape == want_s and codes.get_device() == dev and dev >= 0
+            and scales.get_device() == dev and codes.is_contiguous() and scales.is_contiguous()):
+        _is(codes, f"{name}_codes", u8, want_c, dev)
+        _is(scales, f"{name}_scales", u8, want_s, dev)
 
 
 def _matrices(t: torch.Tensor, name: str):
@@ -606,11 +605,12 @@ def mx_quantize(x: torch.Tensor, fmt: str):
     """(codes, scales) of bf16 x [rows, K] or [G, rows, K] (moe_mx_quantize)."""
     f = _fmt(fmt)
     G, lead, rows, K = _matrices(x, "x")
-    _is(x, "x", torch.bfloat16, (*lead, rows, K))
+    dev = x.get_device()
+    _is(x, "x", torch.bfloat16, (*lead, rows, K), dev)
     codes = (torch.empty_like(x, dtype=torch.uint8) if f == 1 else
              x.new_empty((*lead, rows, K // 2), dtype=torch.uint8))
     scales = x.new_empty((*lead, mx_words(K), rows, 4), dtype=torch.uint8)
-    _call("moe_mx_quantize", x.device, x.data_ptr(), G, rows, K, f, codes.data_ptr(),
+    _call("moe_mx_quantize", dev, x.data_ptr(), G, rows, K, f, codes.data_ptr(),
           scales.data_ptr())
     return codes, scales
 
@@ -620,8 +620,8 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: str) -> torch.
     f = _fmt(fmt)
     G, lead, rows, K = _matrices(codes, "codes")
     K = K if f == 1 else 2 * K
-    _need_mx(codes, scales, "x", lead, rows, K, f)
-    dev = codes.device
+    dev = codes.get_device()
+    _need_mx(codes, scales, "x", lead, rows, K, f, dev)
     x = codes.new_empty((*lead, rows, K), dtype=torch.bfloat16)
     _call("moe_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), G, rows, K, f,
           x.data_ptr())
@@ -642,20 +642,18 @@ def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
     """RMSNorm of x + residual (moe_add_rmsnorm): returns (sum, xn), and with
     ``fmt`` (sum, xn, codes, scales), the MX form of xn.  ``sum_out`` receives
     the sum (x or residual: in place); without a residual the sum is x."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a tensor")
+    dev = _device(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     T, H = x.shape
-    _is(x, "x", torch.bfloat16, (T, H))
+    _is(x, "x", torch.bfloat16, (T, H), dev)
     f = 0 if fmt is None else _fmt(fmt)
     if residual is not None:
-        _is(residual, "residual", torch.bfloat16, (T, H))
+        _is(residual, "residual", torch.bfloat16, (T, H), dev)
     if gamma is not None:
-        _is(gamma, "gamma", torch.float32, (H,))
+        _is(gamma, "gamma", torch.float32, (H,), dev)
     if sum_out is not None:
-        _is(sum_out, "sum_out", torch.bfloat16, (T, H))
-    dev = _one_device(x, residual, gamma, sum_out)
+        _is(sum_out, "sum_out", torch.bfloat16, (T, H), dev)
     total = sum_out
     if total is None:
         total = x if residual is None else torch.empty_like(x)
@@ -677,39 +675,44 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     """Rows grouped by expert times their expert's matrix (moe_grouped_mm): bf16
     x [R,K], w [E,N,K], int32 offsets [E+1] -> bf16 [R,N].  Rows outside the
     groups keep what ``out`` holds (undefined without ``out``)."""
-    if not (isinstance(x, torch.Tensor) and isinstance(w, torch.Tensor)):
-        raise TypeError("x and w must be tensors")
+    dev = _device(x, "x")
+    _device(w, "w")
     if x.dim() != 2 or w.dim() != 3:
         raise ValueError("x must be a matrix and w a stack of matrices")
     R, K = x.shape
     E, N, _ = w.shape
-    _is(x, "x", torch.bfloat16, (R, K))
-    _is(w, "w", torch.bfloat16, (E, N, K))
-    _is(offsets, "offsets", torch.int32, (E + 1,))
+    _is(x, "x", torch.bfloat16, (R, K), dev)
+    _is(w, "w", torch.bfloat16, (E, N, K), dev)
+    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
     if out is None:
         out = x.new_empty((R, N))
     else:
-        _is(out, "out", torch.bfloat16, (R, N))
-    dev = _one_device(x, w, offsets, out, workspace)
+        _is(out, "out", torch.bfloat16, (R, N), dev)
     if workspace is None:
         workspace = x.new_empty(_ws_bytes("moe_grouped_mm_workspace_bytes", R, E, N, K),
                                 dtype=torch.uint8)
+    else:
+        _workspace(workspace, dev)
     _call("moe_grouped_mm", dev, x.data_ptr(), offsets.data_ptr(), R, E, N, K, w.data_ptr(),
           out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
-def _mx_out(R: int, N: int, dev, row_w, row_dest, out, out_rows):
+def _workspace(t, dev: int):
+    if _device(t, "workspace") != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}, got {t.device}")
+
+
+def _mx_out(R: int, N: int, x: torch.Tensor, dev: int, row_w, row_dest, out, out_rows):
     if row_w is not None:
-        _is(row_w, "row_w", torch.float32, (R,))
+        _is(row_w, "row_w", torch.float32, (R,), dev)
     if row_dest is not None:
-        _is(row_dest, "row_dest", torch.int32, (R,))
+        _is(row_dest, "row_dest", torch.int32, (R,), dev)
     if out is None:
-        return torch.empty((R if out_rows is None else out_rows, N), dtype=torch.bfloat16,
-                           device=dev)
+        return x.new_empty((R if out_rows is None else out_rows, N), dtype=torch.bfloat16)
     if out_rows is None:
         out_rows = out.shape[0] if isinstance(out, torch.Tensor) and out.dim() == 2 else R
-    _is(out, "out", torch.bfloat16, (out_rows, N))
+    _is(out, "out", torch.bfloat16, (out_rows, N), dev)
     return out
 
 
@@ -727,13 +730,15 @@ def grouped_mm_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.
     if xl or not wl:
         raise ValueError("x must be a matrix and w a stack of matrices")
     K = kb if f == 1 else 2 * kb
-    _need_mx(x_codes, x_scales, "x", (), R, K, f)
-    _need_mx(w_codes, w_scales, "w", (E,), N, K, f)
-    _is(offsets, "offsets", torch.int32, (E + 1,))
-    y = _mx_out(R, N, x_codes.device, row_w, row_dest, out, out_rows)
-    dev = _one_device(x_codes, w_codes, offsets, row_w, row_dest, y, workspace)
+    dev = x_codes.get_device()
+    _need_mx(x_codes, x_scales, "x", (), R, K, f, dev)
+    _need_mx(w_codes, w_scales, "w", (E,), N, K, f, dev)
+    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
+    y = _mx_out(R, N, x_codes, dev, row_w, row_dest, out, out_rows)
     if workspace is None:
         workspace = y.new_empty(256, dtype=torch.uint8)
+    else:
+        _workspace(workspace, dev)
     _call("moe_grouped_mm_mx", dev, x_codes.data_ptr(), x_scales.data_ptr(), offsets.data_ptr(), R,
           E, N, K, f, w_codes.data_ptr(), w_scales.data_ptr(), _at(row_w), _at(row_dest),
           y.data_ptr(), y.shape[0], workspace.data_ptr(), workspace.numel())
@@ -756,19 +761,22 @@ def expert_rows_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, offsets: torch
     if xl or not wl:
         raise ValueError("x must be a matrix and w13, w2 stacks of matrices")
     H, I = (hb if f == 1 else 2 * hb), I2 // 2
-    _need_mx(x_codes, x_scales, "x", (), T, H, f)
-    _need_mx(w13_codes, w13_scales, "w13", (E,), 2 * I, H, f)
-    _need_mx(w2_codes, w2_scales, "w2", (E,), H, I, f)
-    _is(offsets, "offsets", torch.int32, (E + 1,))
+    dev = x_codes.get_device()
+    _need_mx(x_codes, x_scales, "x", (), T, H, f, dev)
+    _need_mx(w13_codes, w13_scales, "w13", (E,), 2 * I, H, f, dev)
+    _need_mx(w2_codes, w2_scales, "w2", (E,), H, I, f, dev)
+    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
     R = T
     if tok_of is not None:
+        _device(tok_of, "tok_of")
         R = tok_of.numel()
-        _is(tok_of, "tok_of", torch.int32, (R,))
-    y = _mx_out(R, H, x_codes.device, row_w, row_dest, y, y_rows)
-    dev = _one_device(x_codes, offsets, w13_codes, w2_codes, row_dest, row_w, tok_of, y, workspace)
+        _is(tok_of, "tok_of", torch.int32, (R,), dev)
+    y = _mx_out(R, H, x_codes, dev, row_w, row_dest, y, y_rows)
     if workspace is None:
         workspace = y.new_empty(_ws_bytes("moe_expert_rows_mx_workspace_bytes", R, H, E, I, f,
                                           int(tok_of is not None)), dtype=torch.uint8)
+    else:
+        _workspace(workspace, dev)
     _call("moe_expert_rows_mx", dev, x_codes.data_ptr(), x_scales.data_ptr(), T, _at(tok_of),
           offsets.data_ptr(), R, E, H, I, f, w13_codes.data_ptr(), w13_scales.data_ptr(),
           w2_codes.data_ptr(), w2_scales.data_ptr(), _at(row_w), _at(row_dest), y.data_ptr(),

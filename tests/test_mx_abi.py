@@ -133,5 +133,30 @@ def test_python_functions_refuse_host_tensors_and_wrong_layouts():
         ops.grouped_mm(x, None, off)
     with pytest.raises(ValueError):
         ops.grouped_mm(x, w[0], off)
-    with pytest.raises(ValueError, match="must be on"):
-        ops._one_device(x, torch.zeros(1, device="meta"))
+
+
+def test_tensors_of_two_devices_are_refused(monkeypatch):
+    class On(torch.Tensor):  # a host tensor that says it is on a device
+        def get_device(self):
+            return self.on
+
+        @property
+        def is_cuda(self):
+            return True
+
+    def on(dev, *shape, dtype=torch.bfloat16):
+        t = torch.zeros(*shape, dtype=dtype).as_subclass(On)
+        t.on = dev
+        return t
+    called = []
+    monkeypatch.setattr(ops, "_call", lambda *a: called.append(a))
+    ops._is(on(1, 4, 64), "x", torch.bfloat16, (4, 64), 1)
+    with pytest.raises(ValueError, match="cuda:0"):
+        ops._is(on(1, 4, 64), "x", torch.bfloat16, (4, 64), 0)
+    with pytest.raises(ValueError, match="cuda:0"):
+        ops.add_rmsnorm(on(0, 4, 64), on(1, 4, 64))
+    with pytest.raises(ValueError, match="cuda:0"):
+        ops.grouped_mm(on(0, 4, 64), on(1, 2, 64, 64), on(0, 3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="cuda:0"):
+        ops.mx_dequantize(on(0, 4, 64, dtype=torch.uint8), on(1, 1, 4, 4, dtype=torch.uint8), "mxfp8")
+    assert not called
