@@ -608,8 +608,8 @@ def mx_quantize(x: torch.Tensor, fmt: str):
     dev = x.get_device()
     _is(x, "x", torch.bfloat16, (*lead, rows, K), dev)
     codes = (torch.empty_like(x, dtype=torch.uint8) if f == 1 else
-             x.new_empty((*lead, rows, K // 2), dtype=torch.uint8))
-    scales = x.new_empty((*lead, mx_words(K), rows, 4), dtype=torch.uint8)
+             x.new_empty(*lead, rows, K // 2, dtype=torch.uint8))
+    scales = x.new_empty(*lead, mx_words(K), rows, 4, dtype=torch.uint8)
     _call("moe_mx_quantize", dev, x.data_ptr(), G, rows, K, f, codes.data_ptr(),
           scales.data_ptr())
     return codes, scales
@@ -622,7 +622,7 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: str) -> torch.
     K = K if f == 1 else 2 * K
     dev = codes.get_device()
     _need_mx(codes, scales, "x", lead, rows, K, f, dev)
-    x = codes.new_empty((*lead, rows, K), dtype=torch.bfloat16)
+    x = codes.new_empty(*lead, rows, K, dtype=torch.bfloat16)
     _call("moe_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), G, rows, K, f,
           x.data_ptr())
     return x
@@ -661,8 +661,8 @@ def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
     codes = scales = None
     if f:
         codes = (torch.empty_like(x, dtype=torch.uint8) if f == 1 else
-                 x.new_empty((T, H // 2), dtype=torch.uint8))
-        scales = x.new_empty((mx_words(H), T, 4), dtype=torch.uint8)
+                 x.new_empty(T, H // 2, dtype=torch.uint8))
+        scales = x.new_empty(mx_words(H), T, 4, dtype=torch.uint8)
     _call("moe_add_rmsnorm", dev, x.data_ptr(), _at(residual), _at(gamma), float(eps), T, H, f,
           None if total is x and residual is None else total.data_ptr(), xn.data_ptr(),
           _at(codes), _at(scales))
@@ -685,7 +685,7 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     _is(w, "w", torch.bfloat16, (E, N, K), dev)
     _is(offsets, "offsets", torch.int32, (E + 1,), dev)
     if out is None:
-        out = x.new_empty((R, N))
+        out = x.new_empty(R, N)
     else:
         _is(out, "out", torch.bfloat16, (R, N), dev)
     if workspace is None:
@@ -709,7 +709,7 @@ def _mx_out(R: int, N: int, x: torch.Tensor, dev: int, row_w, row_dest, out, out
     if row_dest is not None:
         _is(row_dest, "row_dest", torch.int32, (R,), dev)
     if out is None:
-        return x.new_empty((R if out_rows is None else out_rows, N), dtype=torch.bfloat16)
+        return x.new_empty(R if out_rows is None else out_rows, N, dtype=torch.bfloat16)
     if out_rows is None:
         out_rows = out.shape[0] if isinstance(out, torch.Tensor) and out.dim() == 2 else R
     _is(out, "out", torch.bfloat16, (out_rows, N), dev)
