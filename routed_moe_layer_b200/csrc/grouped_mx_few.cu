@@ -19,6 +19,11 @@
 // Warp roles: warp 0 TMA loads; warp 1 TMEM, scales to TMEM, MMAs; warp 2 the
 // weights' scales (of the gate rows), warp 3 those of the up rows and of the
 // rows; warps 4..7 the epilogue.  Every wait is bounded (common.cuh).
+//
+// HBM bounds it: 1,920 rows, K = 1024, N = 1536, MXFP8: 39.7 us for 216 MB (5.4 TB/s,
+// 0.84 of the measured copy; pair tiles 51 us).  1,536 items on 148 SMs are 10.4
+// rounds, done in 11.  Chunks of 32 rows with the shared memory they free in
+// deeper staging, and of 128 rows, measured the same.
 #include "mx_mma.cuh"
 
 namespace rmoe {
