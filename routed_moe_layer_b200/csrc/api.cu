@@ -682,6 +682,7 @@ MxGemmArgs mx_args(const uint8_t* a_scales, const int32_t* offsets, int32_t R, i
   g.offsets = offsets;
   g.groups = E;
   g.rows = R;
+  g.a_rows = R;
   g.a_scales = reinterpret_cast<const uint32_t*>(a_scales);
   g.b_scales = reinterpret_cast<const uint32_t*>(b_scales);
   g.words = mx_words(K);
@@ -704,6 +705,11 @@ cudaError_t mx_product(int fmt, int epi, const void* a, const void* b, const MxG
   return g.rows <= few * g.groups ? launch_grouped_mx_few(fmt, epi, a, b, g, s)
                                   : launch_grouped_mx(fmt, epi, a, b, g, s);
 }
+
+// Very few rows per expert: the up product loads its rows from the tokens itself,
+// a TMA box a row, instead of from a gathered copy.
+constexpr int64_t GATHER_ROWS_PER_EXPERT = 2;
+bool gather_in_product(int32_t R, int32_t E) { return R <= GATHER_ROWS_PER_EXPERT * (int64_t)E; }
 
 struct MxExpertsLayout {
   size_t x, xs, h, hs, total;
@@ -1266,7 +1272,8 @@ int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int3
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* status = at<int>(workspace, 0);
   const uint8_t *a = x_codes, *as = x_scales;
-  if (tok_of) {  // the tokens' narrow rows in expert order
+  const bool gather = tok_of && (T == 0 || !gather_in_product(R, E));
+  if (gather) {  // the tokens' narrow rows in expert order
     uint8_t* g = at<uint8_t>(workspace, L.x);
     uint8_t* gs = at<uint8_t>(workspace, L.xs);
     RMOE_TRY(launch_gather_mx(x_codes, x_scales, tok_of, T, R, mx_row_bytes(H, fmt), mx_words(H),
@@ -1282,6 +1289,10 @@ int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int3
   up.out = h;
   up.out_scales = reinterpret_cast<uint32_t*>(hs);
   up.clear_status = 1;
+  if (tok_of && !gather) {
+    up.tok_of = tok_of;
+    up.a_rows = T;
+  }
   RMOE_TRY(mx_product(fmt, MX_SWIGLU, a, w13_codes, up, s));
   MxGemmArgs dn = mx_args(hs, offsets, R, E, I, fmt, w2_scales, status);
   dn.n_rows = H;

@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(256)
 
 cudaError_t launch_grouped_mx(int fmt, int epi, const void* a, const void* b, MxGemmArgs args,
                               cudaStream_t stream) {
-  if (args.groups > MX_MAX_GROUPS) return cudaErrorInvalidValue;
+  if (args.groups > MX_MAX_GROUPS || args.tok_of) return cudaErrorInvalidValue;
   CUtensorMap tmA, tmB, tmSB;
   cudaError_t e;
   if ((e = make_tmap_a(&tmA, a, args.rows, args.k_bytes)) != cudaSuccess) return e;

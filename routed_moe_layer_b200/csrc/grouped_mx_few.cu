@@ -94,6 +94,27 @@ __device__ __forceinline__ void tmem_copy_sf(uint32_t taddr, uint64_t sdesc) {
                : "memory");
 }
 
+// The same of the rows in `at` (lane l: those of rows l, l + 32; -1: zeros).
+__device__ __forceinline__ void load_words_at(uint32_t (&v)[SF_WORDS][4], const uint32_t* src,
+                                              size_t pitch, int nw, const int (&at)[CHUNK / 32]) {
+#pragma unroll
+  for (int w = 0; w < SF_WORDS; ++w)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[w][j] = j < CHUNK / 32 && w < nw && at[j] >= 0 ? src[w * pitch + at[j]] : 0u;
+}
+
+// The tokens of an item's rows (lane l: rows l, l + 32); -1: none, or outside [0, T).
+__device__ __forceinline__ void item_tokens(const MxGemmArgs& a, const Tile& t, int lane,
+                                            int (&tok)[CHUNK / 32]) {
+#pragma unroll
+  for (int j = 0; j < CHUNK / 32; ++j) {
+    const int n = lane + 32 * j;
+    tok[j] = n < t.rows ? a.tok_of[t.row0 + n] : -1;
+    if (tok[j] >= a.a_rows) tok[j] = -1;
+  }
+}
+
 // Scale words [w0, w0 + nw) of `rows` rows (`src` + lane + 32 j of each word, `pitch`
 // words from one word to the next) into a buffer: 16-byte row l of a word holds
 // those of rows l, l + 32, l + 64, l + 96.
@@ -112,7 +133,8 @@ __device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[S
   for (int w = 0; w < SF_WORDS; ++w) st_shared_v4(addr + w * MX_SF_BYTES, v[w]);
 }
 
-template <int FMT, int EPI>
+// GATHER: row r of the groups is row tok_of[r] of X, loaded by a TMA box of its own.
+template <int FMT, int EPI, bool GATHER>
 __global__ void __launch_bounds__(THREADS, 1)
     grouped_mx_few_kernel(const __grid_constant__ CUtensorMap tmW,
                           const __grid_constant__ CUtensorMap tmX, const MxGemmArgs args) {
@@ -174,7 +196,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const Tile t = walk.tile(mts, rs);
         const int w_row = t.nt * WM;
         const int nb = (t.rows + XBOX - 1) / XBOX;
-        const uint32_t tx = S::kTiles * W_BYTES + nb * XBOX * KB;
+        const uint32_t tx = S::kTiles * W_BYTES + (GATHER ? t.rows : nb * XBOX) * KB;
+        int tok[CHUNK / 32];
+        if constexpr (GATHER) item_tokens(args, t, lane, tok);
         for (int ks = 0; ks < k_steps; ++ks) {
           if (!__all_sync(FULL, mbar_wait(&st.empty[stage], phase ^ 1u, wc, 71))) {
             ok = false;
@@ -187,8 +211,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int w = 0; w < S::kTiles; ++w)
               tma_load_3d(sx + X_BYTES + w * W_BYTES, &tmW, &st.full[stage], ks * KB,
                           w_row + w * args.b_second, t.g);
-            for (int b = 0; b < nb; ++b)
-              tma_load_2d(sx + b * XBOX * KB, &tmX, &st.full[stage], ks * KB, t.row0 + b * XBOX);
+            if constexpr (!GATHER)
+              for (int b = 0; b < nb; ++b)
+                tma_load_2d(sx + b * XBOX * KB, &tmX, &st.full[stage], ks * KB, t.row0 + b * XBOX);
+          }
+          if constexpr (GATHER) {
+            const bool lead = elect_one();
+            for (int n = 0; n < t.rows; ++n) {
+              const int r = __shfl_sync(FULL, n < 32 ? tok[0] : tok[1], n & 31);
+              // a row past the last one reads zeros
+              if (lead)
+                tma_load_2d(sx + n * KB, &tmX, &st.full[stage], ks * KB, r < 0 ? args.a_rows : r);
+            }
           }
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -295,6 +329,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int item = first; ok && item < total; item += step) {
         if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
         const Tile t = walk.tile(mts, rs);
+        int tok[CHUNK / 32];
+        if constexpr (GATHER)
+          if (warp == 3) item_tokens(args, t, lane, tok);
         for (int w0 = 0; w0 < args.words; w0 += SF_WORDS) {
           const int nw = min(SF_WORDS, args.words - w0);
           const int n0 = t.nt * WM + (warp == 2 ? 0 : args.b_second);  // first weight row
@@ -304,9 +341,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t v[SF_WORDS][4], x[SF_WORDS][4];
           if (warp == 2 || S::kTiles == 2)
             load_words<4>(v, wsrc, args.n_rows, nw, args.n_rows - n0, lane);
-          if (warp == 3)
-            load_words<2>(x, args.a_scales + (size_t)w0 * args.rows + t.row0, args.rows, nw, t.rows,
-                          lane);
+          if (warp == 3) {
+            const uint32_t* xsrc = args.a_scales + (size_t)w0 * args.a_rows;
+            if constexpr (GATHER)
+              load_words_at(x, xsrc, args.a_rows, nw, tok);
+            else
+              load_words<2>(x, xsrc + t.row0, args.a_rows, nw, t.rows, lane);
+          }
           if (!__all_sync(FULL, mbar_wait(&st.sf_empty[buf], phase ^ 1u, wc, 75))) {
             ok = false;
             break;
@@ -442,16 +483,16 @@ cudaError_t make_tmap_matrices(CUtensorMap* map, const void* base, uint64_t grou
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int FMT, int EPI>
+template <int FMT, int EPI, bool GATHER = false>
 cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& args,
                    int grid, cudaStream_t stream) {
   constexpr size_t smem = 1024 + Shape<FMT, EPI>::kOffTail + sizeof(SmemTail);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<int> smem_set[MAX_DEVICES];
   const cudaError_t e =
-      set_smem_limit_per_device(grouped_mx_few_kernel<FMT, EPI>, (int)smem, smem_set);
+      set_smem_limit_per_device(grouped_mx_few_kernel<FMT, EPI, GATHER>, (int)smem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_chained(grouped_mx_few_kernel<FMT, EPI>, dim3(grid), dim3(THREADS), smem, stream,
+  return launch_chained(grouped_mx_few_kernel<FMT, EPI, GATHER>, dim3(grid), dim3(THREADS), smem, stream,
                         tmW, tmX, args);
 }
 
@@ -464,13 +505,21 @@ cudaError_t launch_grouped_mx_few(int fmt, int epi, const void* a, const void* b
   cudaError_t e;
   if ((e = make_tmap_matrices(&tmW, b, args.groups, args.n_rows, args.k_bytes)) != cudaSuccess)
     return e;
-  if ((e = make_tmap_rows(&tmX, a, args.rows, args.k_bytes, XBOX)) != cudaSuccess) return e;
+  if ((e = make_tmap_rows(&tmX, a, args.a_rows, args.k_bytes, args.tok_of ? 1 : XBOX)) !=
+      cudaSuccess)
+    return e;
   args.n_out_tile = WM;
   args.n_tiles = (args.n_valid + WM - 1) / WM;
   args.b_second = args.n_valid;  // MX_SWIGLU: the up rows
   const long long items = ((long long)args.rows / CHUNK + args.groups) * args.n_tiles;
   const int sms = num_sms();
   const int grid = (int)(items < sms ? items : sms);
+  if (args.tok_of) {
+    if (epi != MX_SWIGLU) return cudaErrorInvalidValue;
+    return fmt == MOE_MXFP8
+               ? launch<MOE_MXFP8, MX_SWIGLU, true>(tmW, tmX, args, grid, stream)
+               : launch<MOE_MXFP4, MX_SWIGLU, true>(tmW, tmX, args, grid, stream);
+  }
   if (fmt == MOE_MXFP8)
     return epi == MX_SWIGLU ? launch<MOE_MXFP8, MX_SWIGLU>(tmW, tmX, args, grid, stream)
                             : launch<MOE_MXFP8, MX_ROWS>(tmW, tmX, args, grid, stream);

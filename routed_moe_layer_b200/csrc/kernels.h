@@ -216,8 +216,11 @@ enum MxEpi { MX_ROWS = 0, MX_SWIGLU = 1 };
 struct MxGemmArgs {
   const int* offsets;        // [groups+1] device: first row of each group
   int groups;
-  int rows;                  // rows of A: no group reaches past them
-  const uint32_t* a_scales;  // [words][rows]
+  int rows;                  // rows of the groups: no group reaches past them
+  int a_rows;                // rows of A: rows, or with tok_of those it is gathered from
+  const int* tok_of;         // [rows] row of A of each row, or null for the row itself
+                             //   (MX_SWIGLU with few rows per group only)
+  const uint32_t* a_scales;  // [words][a_rows]
   const uint32_t* b_scales;  // [groups][words][n_rows]
   int n_rows;                // weight rows per group: N, or 2I (MX_SWIGLU)
   int words;                 // scale words per row
@@ -234,7 +237,7 @@ struct MxGemmArgs {
   int n_tiles, n_out_tile, b_second;  // set by the launchers
 };
 
-// a: codes [rows, k_bytes]; b: codes [groups, n_rows, k_bytes].
+// a: codes [a_rows, k_bytes]; b: codes [groups, n_rows, k_bytes].
 cudaError_t launch_grouped_mx(int fmt, int epi, const void* a, const void* b, MxGemmArgs args,
                               cudaStream_t stream);
 // The same for few rows per group (grouped_mx_few.cu).

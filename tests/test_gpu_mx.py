@@ -405,7 +405,7 @@ def nearest(v, like, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 4, 64, 32), (9, 4, 2, 160, 96), (70, 16, 4, 256, 160),
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 4, 64, 32), (30, 32, 4, 288, 160), (13, 16, 3, 1184, 64), (9, 4, 2, 160, 96), (70, 16, 4, 256, 160),
                                        (400, 3, 2, 512, 288), (333, 1, 1, 96, 128)])
 def test_expert_rows_mx(T, E, k, H, I, fmt):
     xc, xs, x = operands(T, H, fmt, T + H)
