@@ -699,10 +699,13 @@ MxGemmArgs mx_args(const uint8_t* a_scales, const int32_t* offsets, int32_t R, i
 // four epilogue warps more: MXFP8 15 rows 54.4 / 59.7, 24 rows 59.0 / 61.1, 32 rows
 // 66.6 / 60.8; MXFP4 (whose weights stream in half the time) 15 rows 41.3 / 43.9,
 // 24 rows 48.4 / 44.5.
+bool mx_few(int fmt, int epi, int64_t rows, int64_t groups) {
+  return rows <= (epi == MX_SWIGLU ? 64 : fmt == MOE_MXFP8 ? 24 : 16) * groups;
+}
+
 cudaError_t mx_product(int fmt, int epi, const void* a, const void* b, const MxGemmArgs& g,
                        cudaStream_t s) {
-  const int64_t few = epi == MX_SWIGLU ? 64 : fmt == MOE_MXFP8 ? 24 : 16;
-  return g.rows <= few * g.groups ? launch_grouped_mx_few(fmt, epi, a, b, g, s)
+  return mx_few(fmt, epi, g.rows, g.groups) ? launch_grouped_mx_few(fmt, epi, a, b, g, s)
                                   : launch_grouped_mx(fmt, epi, a, b, g, s);
 }
 
@@ -1301,6 +1304,7 @@ int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int3
   dn.row_dest = row_dest;
   dn.out_rows = y_rows;
   dn.out = y;
+  dn.after_up = mx_few(fmt, MX_SWIGLU, R, E) ? 1 : 0;
   return cuda_status(mx_product(fmt, MX_ROWS, h, w2_codes, dn, s));
 }
 

@@ -145,7 +145,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   SmemTail& st = *reinterpret_cast<SmemTail*>(smem + S::kOffTail);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&st.full[s], 1);
@@ -169,7 +168,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(&st.tmem_base, TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_wait();  // what comes before reads nothing that an earlier kernel writes
+  // What comes before reads nothing that an earlier kernel writes.  After the up
+  // product (args.after_up) only its rows have to be waited for: it lets this
+  // kernel start when all that came before it was complete, so the group table
+  // and the weights can be read while it runs.
+  const bool early = EPI == MX_ROWS && args.after_up != 0;
+  if (!early) pdl_wait();
+  pdl_launch_dependents();  // not before pdl_wait: the kernel after may be such a one
   const int total = mx_group_table<CHUNK>(args, st.groups) * args.n_tiles;
   tc_fence_before_sync();
   __syncthreads();
@@ -191,6 +196,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_parity = 0;
       bool ok = true;
+      int ahead = 0;  // steps of the first item whose weights are loaded before the rows
       for (int item = first; ok && item < total; item += step) {
         if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
         const Tile t = walk.tile(mts, rs);
@@ -199,6 +205,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t tx = S::kTiles * W_BYTES + (GATHER ? t.rows : nb * XBOX) * KB;
         int tok[CHUNK / 32];
         if constexpr (GATHER) item_tokens(args, t, lane, tok);
+        auto load_weights = [&](int st_i, int ks) {  // one lane
+          uint8_t* sw = smem + (size_t)st_i * S::kStageBytes + X_BYTES;
+          mbar_arrive_expect_tx(&st.full[st_i], tx);
+#pragma unroll
+          for (int w = 0; w < S::kTiles; ++w)
+            tma_load_3d(sw + w * W_BYTES, &tmW, &st.full[st_i], ks * KB,
+                        w_row + w * args.b_second, t.g);
+        };
+        if (early && item == first) {
+          ahead = min(S::kStages, k_steps);
+          if (elect_one())
+            for (int ks = 0; ks < ahead; ++ks) load_weights(ks, ks);
+          __syncwarp();
+          pdl_wait();
+        }
         for (int ks = 0; ks < k_steps; ++ks) {
           if (!__all_sync(FULL, mbar_wait(&st.empty[stage], phase ^ 1u, wc, 71))) {
             ok = false;
@@ -206,15 +227,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           uint8_t* sx = smem + (size_t)stage * S::kStageBytes;
           if (elect_one()) {
-            mbar_arrive_expect_tx(&st.full[stage], tx);
-#pragma unroll
-            for (int w = 0; w < S::kTiles; ++w)
-              tma_load_3d(sx + X_BYTES + w * W_BYTES, &tmW, &st.full[stage], ks * KB,
-                          w_row + w * args.b_second, t.g);
+            if (ahead == 0) load_weights(stage, ks);
             if constexpr (!GATHER)
               for (int b = 0; b < nb; ++b)
                 tma_load_2d(sx + b * XBOX * KB, &tmX, &st.full[stage], ks * KB, t.row0 + b * XBOX);
           }
+          if (ahead > 0) --ahead;
           if constexpr (GATHER) {
             const bool lead = elect_one();
             for (int n = 0; n < t.rows; ++n) {
@@ -323,6 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
     } else if (warp < EPI_WARP0) {
       // ------------------------------------------------ scales (warp 2: weight tile 0; 3: the rest)
+      if (early && warp == 3) pdl_wait();
       int buf = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -364,6 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     } else {
       // ------------------------------------------------ epilogue warps 4..7
+      if (early) pdl_wait();
       const int q = warp & 3;
       int acc = 0;
       uint32_t acc_phase = 0;
@@ -457,6 +477,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 
+  // no CTA ends before the kernels that came before have: what follows this kernel
+  // relies on that
+  pdl_wait();
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 1) {

@@ -233,6 +233,8 @@ struct MxGemmArgs {
   uint32_t* out_scales;      // MX_SWIGLU: [mx_words(I)][rows]
   int* status;
   int clear_status;          // 1: the status word is cleared first
+  int after_up;              // 1: the kernel before on the stream is the few-rows product that
+                             //   writes a (launch_grouped_mx_few): weights are read ahead of it
   unsigned long long timeout_ns;
   int n_tiles, n_out_tile, b_second;  // set by the launchers
 };
