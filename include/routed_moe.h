@@ -368,8 +368,8 @@ MOE_API int32_t moe_rmsnorm(const void* x, const float* gamma, float eps, int32_
  * A stack of matrices [G, rows, K] has G such arrays of each, one after the
  * other.  K is a multiple of 32 (<= 16384).  codes, bf16 inputs, xn and
  * the scales of weights are 16-byte aligned, bf16 outputs of products and what
- * is quantised or dequantised 32-byte, the scales of rows 4-byte
- * (MOE_ERR_INVALID_ARG).  Forward only, like the block itself. */
+ * is quantised or dequantised 32-byte, the scales of rows, offsets, indices and
+ * row weights 4-byte (MOE_ERR_INVALID_ARG).  Forward only, like the block itself. */
 typedef enum {
   MOE_MXFP8 = 1, /* E4M3 elements */
   MOE_MXFP4 = 2  /* E2M1 elements */
@@ -428,7 +428,9 @@ MOE_API int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R,
  *   row_dest device int32 [R], distinct rows of y, or NULL (dest(r) = r); a row
  *            whose destination lies outside [0, y_rows) is not stored
  *   y        device bf16 [y_rows, N] (y_rows >= R without row_dest)
- * Offsets, sizes, errors and workspace as moe_grouped_mm. */
+ * Offsets, sizes, errors and workspace as moe_grouped_mm.  A row's bits do not
+ * depend on the other rows of the call (the kernels for few and for many rows
+ * per expert give the same). */
 MOE_API int32_t moe_grouped_mm_mx(const uint8_t* x_codes, const uint8_t* x_scales,
                                   const int32_t* offsets, int32_t R, int32_t E, int32_t N,
                                   int32_t K, int32_t fmt, const uint8_t* w_codes,

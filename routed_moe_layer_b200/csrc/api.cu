@@ -1168,7 +1168,8 @@ int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R, int32_t
   if (st != MOE_OK) return st;
   if (R == 0) return MOE_OK;
   if (!x || !offsets || !w || !y || y == x || y == w) return MOE_ERR_INVALID_ARG;
-  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 32)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 32) || !aligned(offsets, 4))
+    return MOE_ERR_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, moe_grouped_mm_workspace_bytes(R, E, N, K)))
     return MOE_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1229,7 +1230,8 @@ int32_t moe_grouped_mm_mx(const uint8_t* x_codes, const uint8_t* x_scales, const
     return MOE_ERR_INVALID_ARG;
   if (!row_dest && y_rows < R) return MOE_ERR_INVALID_ARG;
   if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(y, 32) || !aligned(x_scales, 4) ||
-      !aligned(w_scales, 16))
+      !aligned(w_scales, 16) || !aligned(offsets, 4) || !aligned(row_w, 4) ||
+      !aligned(row_dest, 4))
     return MOE_ERR_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, moe_grouped_mm_mx_workspace_bytes(R, E, N, K)))
     return MOE_ERR_WORKSPACE;
@@ -1268,7 +1270,8 @@ int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int3
   if ((!tok_of && T != R) || (!row_dest && y_rows < R)) return MOE_ERR_INVALID_ARG;
   if (!aligned(x_codes, 16) || !aligned(w13_codes, 16) || !aligned(w2_codes, 16) ||
       !aligned(y, 32) || !aligned(x_scales, 4) || !aligned(w13_scales, 16) ||
-      !aligned(w2_scales, 16))
+      !aligned(w2_scales, 16) || !aligned(offsets, 4) || !aligned(tok_of, 4) ||
+      !aligned(row_w, 4) || !aligned(row_dest, 4))
     return MOE_ERR_INVALID_ARG;
   const MxExpertsLayout L = mx_experts_layout(R, H, I, fmt, tok_of != nullptr);
   if (!ws_ok(workspace, workspace_bytes, L.total)) return MOE_ERR_WORKSPACE;

@@ -430,6 +430,28 @@ def test_expert_rows_mx(T, E, k, H, I, fmt):
     assert torch.equal(y2, y[order.to(DEV)])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_rows_bits_do_not_depend_on_the_other_rows(fmt):
+    """The forms for few and for many rows per expert, with and without a gathered
+    copy: every row has the same bits in a call of 3, 40 and 700 rows."""
+    E, H, I, R = 2, 288, 160, 700
+    xc, xs, _ = operands(R, H, fmt, 1)
+    w13c, w13s, _ = operands(2 * I, H, fmt, 2, lead=E, scale=H ** -0.5)
+    w2c, w2s, _ = operands(H, I, fmt, 3, lead=E, scale=I ** -0.5)
+    rows = torch.arange(R, dtype=torch.int32, device=DEV)
+
+    def call(lo, mid, hi):  # rows [lo, mid) with expert 0, [mid, hi) with expert 1
+        off = torch.tensor([0, mid - lo, hi - lo], dtype=torch.int32, device=DEV)
+        y = ops.expert_rows_mx(xc, xs, off, w13c, w13s, w2c, w2s, None, fmt, tok_of=rows[lo:hi])
+        z = ops.grouped_mm_mx(xc[lo:hi].contiguous(), xs[:, lo:hi].contiguous(), w13c, w13s, off, fmt)
+        return y, z
+    full = call(0, 300, R)
+    for lo, mid, hi in ((298, 300, 301), (290, 300, 330), (0, 300, 400)):
+        part = call(lo, mid, hi)
+        for a, b in zip(part, full):
+            assert torch.equal(a, b[lo:hi])
+
+
 def test_expert_rows_mx_token_outside_counts_as_zeros():
     xc, xs, _ = operands(4, 64, "mxfp8", 1)
     w13c, w13s, _ = operands(64, 64, "mxfp8", 2, lead=2)

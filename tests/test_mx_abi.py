@@ -63,7 +63,7 @@ GROUPED = [
     ({"N": 16416}, SHAPE), ({"K": 16416}, SHAPE), ({"R": 2 ** 31 - 1}, SHAPE),
     ({"x": 0}, INVALID), ({"w": 0}, INVALID), ({"off": 0}, INVALID), ({"y": 0}, INVALID),
     ({"y": P}, INVALID), ({"y": 2 * P}, INVALID), ({"x": P + 8}, INVALID),
-    ({"w": 2 * P + 8}, INVALID), ({"y": 3 * P + 16}, INVALID),
+    ({"w": 2 * P + 8}, INVALID), ({"y": 3 * P + 16}, INVALID), ({"off": 4 * P + 2}, INVALID),
     ({"ws": 0}, WORKSPACE), ({"ws": 5 * P + 64}, WORKSPACE), ({"ws_bytes": 128}, WORKSPACE),
 ]
 
@@ -96,6 +96,7 @@ def test_grouped_mm_mx_checks(L, kw, expect):
     ({"H": 100}, SHAPE), ({"I": 33}, SHAPE), ({"fmt": 7}, INVALID), ({"w2": 0}, INVALID),
     ({"w2s": 0}, INVALID), ({"tok": 0}, INVALID),      # rows not gathered, but T != R
     ({"dest": 0, "y_rows": 5}, INVALID), ({"w13": 9 * P + 8}, INVALID),
+    ({"tok": 3 * P + 1}, INVALID), ({"dest": 8 * P + 2}, INVALID), ({"w2s": 7 * P + 4}, INVALID),
     ({"y": 10 * P + 16}, INVALID), ({"ws_bytes": 64}, WORKSPACE), ({"ws": 0}, WORKSPACE),
 ])
 def test_expert_rows_mx_checks(L, kw, expect):
