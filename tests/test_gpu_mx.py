@@ -313,6 +313,48 @@ def test_every_element_and_scale_reaches_the_product(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R", [24, 96])  # swapped operands, pair tiles
+def test_powers_far_from_each_other(R, fmt):
+    """Blocks of rows with powers from 2^-126 to 2^120 against columns with the
+    opposite ones: each product lies near 1 and is exact, however far its
+    factors' scales lie apart."""
+    K, N = 256, 64
+    rng = np.random.default_rng(5)
+    one = 0x38 if fmt == "mxfp8" else 2  # 1.0
+    xc, wc = np.full((R, K), one, np.uint8), np.full((N, K), one, np.uint8)
+    blocks = K // 32
+    # one nonzero block a row; in it the row's power p, and the columns' -p in that block
+    p = rng.integers(-120, 121, blocks)
+    at = np.arange(R) % blocks
+    xc[np.arange(K)[None, :] // 32 != at[:, None]] = 0
+    xsb = np.full((R, blocks), 127, np.uint8)
+    xsb[np.arange(R), at] = 127 + p[at]
+    wsb = np.broadcast_to(127 - p, (N, blocks)).astype(np.uint8) + rng.integers(0, 5, (N, blocks)).astype(np.uint8)
+    xd, xsd = stored(xc, xsb, fmt)
+    wd, wsd = stored(wc, wsb, fmt)
+    off = torch.tensor([0, R], dtype=torch.int32, device=DEV)
+    y = ops.grouped_mm_mx(xd.to(DEV), xsd.to(DEV), wd[None].to(DEV), wsd[None].to(DEV), off, fmt)
+    ref = 32.0 * 2.0 ** (wsb.astype(int) - (127 - p))[:, at].T
+    assert np.array_equal(to_np(y), ref)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_one_expert_takes_every_row(fmt):
+    """Skewed as far as it goes: the forms are chosen by the average."""
+    E, H, I = 64, 160, 64
+    w13c, w13s, w13 = operands(2 * I, H, fmt, 2, lead=E, scale=H ** -0.5)
+    w2c, w2s, w2 = operands(H, I, fmt, 3, lead=E, scale=I ** -0.5)
+    for R, e in ((100, 63), (100, 0), (900, 31), (1500, 7)):
+        xc, xs, x = operands(R, H, fmt, R)
+        off = np.where(np.arange(E + 1) > e, R, 0).astype(np.int32)
+        tok = torch.randperm(R, generator=gen(1)).int()
+        ref, tol = experts_tolerance(x[tok.numpy()], w13, w2, off, fmt, np.ones(R))
+        y = ops.expert_rows_mx(xc, xs, torch.from_numpy(off).to(DEV), w13c, w13s, w2c, w2s, None,
+                               fmt, tok_of=tok.to(DEV))
+        assert np.all(np.abs(to_np(y) - ref) <= tol * (1 + 1e-6))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_nan_blocks_reach_their_rows_and_columns_alone(fmt):
     R, N, K = 200, 96, 160
     xc, xs, _ = operands(R, K, fmt, 3)
@@ -523,8 +565,9 @@ def test_forward_mx_is_its_steps(Is):
     assert (full - ref).float().norm() < 0.2 * ref.float().norm()
 
 
-def test_captured_replayed_and_on_two_streams():
-    T, H, E, I, k = 96, 512, 16, 128, 4
+@pytest.mark.parametrize("T", [6, 32, 96])  # rows from the tokens, swapped products, pair tiles
+def test_captured_replayed_and_on_two_streams(T):
+    H, E, I, k = 512, 16, 128, 4
     cfg, d = block(T, H, E, I, 0, k, 6)
     w13, w2 = ops.mx_quantize(d["w13"], "mxfp4"), ops.mx_quantize(d["w2"], "mxfp4")
     res = inputs.make_tokens(T, H, seed=3).to(DEV)
