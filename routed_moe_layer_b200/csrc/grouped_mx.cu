@@ -194,31 +194,13 @@ __device__ __forceinline__ void load_part(uint32_t tb, int part, uint32_t (&v)[E
   tmem_ld_wait();
 }
 
-// Named barrier of the four epilogue warps that share a TMEM lane quarter.
-__device__ __forceinline__ void quarter_sync(int q) {
-  asm volatile("bar.sync %0, 128;" ::"r"(q + 1) : "memory");
-}
-
 // Whether a tile's wait has come to its end in all the epilogue warps that work
 // together (MX_ROWS: those of a quarter, which share barriers): they leave the
 // tile loop together when it has run out in one.
 template <int EPI>
 __device__ __forceinline__ bool epilogue_agrees(int q, bool ok) {
   if constexpr (EPI == MX_SWIGLU) return ok;
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, r;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-      "bar.red.and.pred r, %1, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}\n"
-      : "=r"(all)
-      : "r"(q + 1), "r"(static_cast<uint32_t>(ok))
-      : "memory");
-  return all != 0;
-}
-
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
-               "r"(bytes)
-               : "memory");
+  return four_warps_agree(q + 1, ok);
 }
 
 // t: this CTA's part of the tile; out: the tile's rows in shared memory (MX_ROWS).
@@ -241,7 +223,7 @@ __device__ __forceinline__ void store_part(const MxGemmArgs& a, const uint32_t (
       if (dest >= a.out_rows) dest = -1;
     }
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last tile's copies
-    quarter_sync(q);
+    four_warps_sync(q + 1);
 #pragma unroll
     for (int k = 0; k < EPI_COLS / 8; ++k) {
       uint32_t pk[4];
@@ -254,7 +236,7 @@ __device__ __forceinline__ void store_part(const MxGemmArgs& a, const uint32_t (
       st_shared_v4(out + r_in_tile * OUT_PITCH + part * (EPI_COLS * 2) + 16 * k, pk);
     }
     fence_proxy_async_smem();  // these writes -> the copies
-    quarter_sync(q);
+    four_warps_sync(q + 1);
     if (dest >= 0)
       bulk_store(static_cast<__nv_bfloat16*>(a.out) + (size_t)dest * a.n_valid + t.nt * BN,
                  out + crow * OUT_PITCH, 2 * min(BN, a.n_valid - t.nt * BN));

@@ -31,30 +31,34 @@ namespace rmoe {
 namespace {
 
 constexpr int WM = 128;           // weight rows per item (the MMA's M)
-constexpr int CHUNK = 64;         // rows per item (the MMA's N, padded to 16)
+constexpr long long WIDE_ROWS = 32;
 constexpr int KB = 128;           // bytes of a row per K step
 constexpr int XBOX = 32;          // rows per TMA box
 constexpr int W_BYTES = WM * KB;
-constexpr int X_BYTES = CHUNK * KB;
+constexpr int OUT_PITCH = 2 * WM; // bytes of an output row in shared memory
 constexpr int THREADS = 256;
 constexpr int EPI_WARP0 = 4;
 constexpr int EPI_WARPS = 4;
 constexpr int SF_WORDS = 8;       // words per row in a buffer of scales
-constexpr int MAX_STAGES = 8;
+constexpr int MAX_STAGES = 6;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t ACC_COLS = 128;   // per accumulator buffer: (gate,) up or rows, 64 each
-constexpr uint32_t TMEM_SF = 256;    // + 32 per stage: 4 per word of each tile, rows first
 
-template <int FMT, int EPI>
+// C: rows per item at most (the MMA's N, padded to 16).
+template <int FMT, int EPI, int C>
 struct Shape {
   static constexpr int kWords = FMT == MOE_MXFP8 ? 1 : 2;  // scale words per row and K step
   static constexpr int kTiles = EPI == MX_SWIGLU ? 2 : 1;  // weight tiles per item
-  static constexpr int kStageBytes = kTiles * W_BYTES + X_BYTES;
-  static constexpr int kStages = EPI == MX_SWIGLU ? 4 : 8;
+  static constexpr int kXBytes = C * KB;
+  static constexpr int kStageBytes = kTiles * W_BYTES + kXBytes;
+  static constexpr int kStages = EPI == MX_SWIGLU ? 4 : C == 64 ? 6 : 5;
+  static constexpr uint32_t kAcc = kTiles * C;   // TMEM columns of an accumulator (gate, up)
+  static constexpr uint32_t kTmemSf = 2 * kAcc;  // + 32 per stage: 4 per word of each tile, rows first
   static constexpr int kSfBytes = SF_WORDS * MX_SF_BYTES;  // per operand tile and buffer
   static constexpr int kSfBuf = (kTiles + 1) * kSfBytes;   // the rows', then the weights'
   static constexpr int kOffSf = kStages * kStageBytes;
-  static constexpr int kOffTail = kOffSf + 2 * kSfBuf;
+  static constexpr int kOffOut = kOffSf + 2 * kSfBuf;
+  static constexpr int kOffTail = kOffOut + (EPI == MX_ROWS ? C * OUT_PITCH : 0);
+  static_assert(kStages <= MAX_STAGES && kTmemSf + 32 * kStages <= TMEM_COLS, "TMEM");
 };
 
 struct __align__(8) SmemTail {
@@ -94,21 +98,23 @@ __device__ __forceinline__ void tmem_copy_sf(uint32_t taddr, uint64_t sdesc) {
                : "memory");
 }
 
-// The same of the rows in `at` (lane l: those of rows l, l + 32; -1: zeros).
+// The same of the rows in `at` (lane l: those of rows l, l + 32, ..; -1: zeros).
+template <int J>
 __device__ __forceinline__ void load_words_at(uint32_t (&v)[SF_WORDS][4], const uint32_t* src,
-                                              size_t pitch, int nw, const int (&at)[CHUNK / 32]) {
+                                              size_t pitch, int nw, const int (&at)[J]) {
 #pragma unroll
   for (int w = 0; w < SF_WORDS; ++w)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      v[w][j] = j < CHUNK / 32 && w < nw && at[j] >= 0 ? src[w * pitch + at[j]] : 0u;
+      v[w][j] = j < J && w < nw && at[j] >= 0 ? src[w * pitch + at[j]] : 0u;
 }
 
-// The tokens of an item's rows (lane l: rows l, l + 32); -1: none, or outside [0, T).
+// The tokens of an item's rows (lane l: rows l, l + 32, ..); -1: none, or outside [0, T).
+template <int J>
 __device__ __forceinline__ void item_tokens(const MxGemmArgs& a, const Tile& t, int lane,
-                                            int (&tok)[CHUNK / 32]) {
+                                            int (&tok)[J]) {
 #pragma unroll
-  for (int j = 0; j < CHUNK / 32; ++j) {
+  for (int j = 0; j < J; ++j) {
     const int n = lane + 32 * j;
     tok[j] = n < t.rows ? a.tok_of[t.row0 + n] : -1;
     if (tok[j] >= a.a_rows) tok[j] = -1;
@@ -133,12 +139,25 @@ __device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[S
   for (int w = 0; w < SF_WORDS; ++w) st_shared_v4(addr + w * MX_SF_BYTES, v[w]);
 }
 
+__device__ __forceinline__ void st_shared_b16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+
+// v[n / 32], n the same in all lanes.
+template <typename V, int J>
+__device__ __forceinline__ V of_row(const V (&v)[J], int n) {
+  V r = v[0];
+#pragma unroll
+  for (int j = 1; j < J; ++j) r = n >= 32 * j ? v[j] : r;
+  return r;
+}
+
 // GATHER: row r of the groups is row tok_of[r] of X, loaded by a TMA box of its own.
-template <int FMT, int EPI, bool GATHER>
+template <int FMT, int EPI, int C, bool GATHER>
 __global__ void __launch_bounds__(THREADS, 1)
     grouped_mx_few_kernel(const __grid_constant__ CUtensorMap tmW,
                           const __grid_constant__ CUtensorMap tmX, const MxGemmArgs args) {
-  using S = Shape<FMT, EPI>;
+  using S = Shape<FMT, EPI, C>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -175,7 +194,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const bool early = EPI == MX_ROWS && args.after_up != 0;
   if (!early) pdl_wait();
   pdl_launch_dependents();  // not before pdl_wait: the kernel after may be such a one
-  const int total = mx_group_table<CHUNK>(args, st.groups) * args.n_tiles;
+  const int total = mx_group_table<C>(args, st.groups) * args.n_tiles;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -187,7 +206,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int* mts = st.groups.mt_start;
     const int* rs = st.groups.row_start;
     const int dm = step / args.n_tiles, dn = step - dm * args.n_tiles;
-    TileWalk<CHUNK> walk;
+    TileWalk<C> walk;
     walk.start(first, args.n_tiles, args.groups, mts);
     const uint32_t smem0 = smem_u32(smem), sf0 = smem0 + S::kOffSf;
 
@@ -203,10 +222,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int w_row = t.nt * WM;
         const int nb = (t.rows + XBOX - 1) / XBOX;
         const uint32_t tx = S::kTiles * W_BYTES + (GATHER ? t.rows : nb * XBOX) * KB;
-        int tok[CHUNK / 32];
+        int tok[C / 32];
         if constexpr (GATHER) item_tokens(args, t, lane, tok);
         auto load_weights = [&](int st_i, int ks) {  // one lane
-          uint8_t* sw = smem + (size_t)st_i * S::kStageBytes + X_BYTES;
+          uint8_t* sw = smem + (size_t)st_i * S::kStageBytes + S::kXBytes;
           mbar_arrive_expect_tx(&st.full[st_i], tx);
 #pragma unroll
           for (int w = 0; w < S::kTiles; ++w)
@@ -236,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if constexpr (GATHER) {
             const bool lead = elect_one();
             for (int n = 0; n < t.rows; ++n) {
-              const int r = __shfl_sync(FULL, n < 32 ? tok[0] : tok[1], n & 31);
+              const int r = __shfl_sync(FULL, of_row(tok, n), n & 31);
               // a row past the last one reads zeros
               if (lead)
                 tma_load_2d(sx + n * KB, &tmX, &st.full[stage], ks * KB, r < 0 ? args.a_rows : r);
@@ -267,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
         const Tile t = walk.tile(mts, rs);
         const uint32_t idesc = idesc_mx<FMT>(WM, (t.rows + 15) & ~15);
-        const uint32_t d = tmem_base + acc * ACC_COLS;
+        const uint32_t d = tmem_base + acc * S::kAcc;
         int chunk_left = 0;
         uint64_t dsf = dsf0;
         for (int ks = 0; ks < k_steps; ++ks) {
@@ -286,7 +305,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_fence_after_sync();
           --chunk_left;
           const bool chunk_done = chunk_left == 0 || ks + 1 == k_steps;
-          const uint32_t sf = tmem_base + TMEM_SF + 32 * stage;
+          const uint32_t sf = tmem_base + S::kTmemSf + 32 * stage;
           const uint64_t dx = dx0 + static_cast<uint64_t>(stage * (S::kStageBytes >> 4));
           if (elect_one()) {
 #pragma unroll
@@ -312,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t id = idesc_sf(idesc, FMT == MOE_MXFP8 ? kk : 2 * (kk & 1));
 #pragma unroll
                 for (int w = 0; w < S::kTiles; ++w)
-                  umma_mx<FMT>(d + w * CHUNK, dx + ((X_BYTES + w * W_BYTES) >> 4) + 2 * kk,
+                  umma_mx<FMT>(d + w * C, dx + ((S::kXBytes + w * W_BYTES) >> 4) + 2 * kk,
                                dx + 2 * kk, id, sf + 4 * S::kWords * (1 + w) + word, sf + word,
                                (ks | kk) != 0 ? 1u : 0u);
               }
@@ -348,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int item = first; ok && item < total; item += step) {
         if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
         const Tile t = walk.tile(mts, rs);
-        int tok[CHUNK / 32];
+        int tok[C / 32];
         if constexpr (GATHER)
           if (warp == 3) item_tokens(args, t, lane, tok);
         for (int w0 = 0; w0 < args.words; w0 += SF_WORDS) {
@@ -365,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if constexpr (GATHER)
               load_words_at(x, xsrc, args.a_rows, nw, tok);
             else
-              load_words<2>(x, xsrc + t.row0, args.a_rows, nw, t.rows, lane);
+              load_words<C / 32>(x, xsrc + t.row0, args.a_rows, nw, t.rows, lane);
           }
           if (!__all_sync(FULL, mbar_wait(&st.sf_empty[buf], phase ^ 1u, wc, 75))) {
             ok = false;
@@ -385,32 +404,37 @@ __global__ void __launch_bounds__(THREADS, 1)
       // ------------------------------------------------ epilogue warps 4..7
       if (early) pdl_wait();
       const int q = warp & 3;
+      constexpr int COPIES = C / EPI_WARPS;  // MX_ROWS: rows that a warp copies, one a lane
+      const uint32_t out = smem0 + S::kOffOut;
       int acc = 0;
       uint32_t acc_phase = 0;
       for (int item = first; item < total; item += step) {
         if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
         const Tile t = walk.tile(mts, rs);
         const int col0 = t.nt * WM + q * 32;  // the warp's first output column
-        // MX_ROWS: lane l holds output row (-1: none) and weight of rows l, l + 32
-        int dest[CHUNK / 32];
-        float w[CHUNK / 32];
+        const int crow = q * COPIES + lane;   // MX_ROWS: this lane's row of the copies,
+        int dest = -1;                        // its output row (-1: none),
+        float w[C / 32];                      // and the weights of rows l, l + 32, ..
         if constexpr (EPI == MX_ROWS) {
+          if (lane < COPIES && crow < t.rows) {
+            dest = args.row_dest ? args.row_dest[t.row0 + crow] : t.row0 + crow;
+            if (dest >= args.out_rows) dest = -1;
+          }
 #pragma unroll
-          for (int j = 0; j < CHUNK / 32; ++j) {
-            const int n = lane + 32 * j, row = t.row0 + n;
-            dest[j] = -1;
-            w[j] = 1.0f;
-            if (n < t.rows && col0 < args.n_valid) {
-              dest[j] = args.row_dest ? args.row_dest[row] : row;
-              if (dest[j] >= args.out_rows) dest[j] = -1;
-              if (args.row_w) w[j] = args.row_w[row];
-            }
+          for (int j = 0; j < C / 32; ++j) {
+            const int n = lane + 32 * j;
+            w[j] = args.row_w && n < t.rows ? args.row_w[t.row0 + n] : 1.0f;
           }
         }
-        if (!__all_sync(FULL, mbar_wait(&st.tfull[acc], acc_phase, wc, 76))) break;
+        bool ok = __all_sync(FULL, mbar_wait(&st.tfull[acc], acc_phase, wc, 76));
+        if constexpr (EPI == MX_ROWS) {
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last item's copies
+          ok = four_warps_agree(1, ok);
+        }
+        if (!ok) break;
         tc_fence_after_sync();
         const uint32_t tb =
-            tmem_base + acc * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
+            tmem_base + acc * S::kAcc + (static_cast<uint32_t>(q * 32) << 16);
         // 16 rows at a time, without branches between them: their shuffles,
         // reductions and stores overlap (row by row they cost 170 cycles each,
         // and bounded the call from 8 rows a group on)
@@ -419,20 +443,22 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t g[16];
           tmem_ld_32x32b_x16(tb + n0, g);
           if constexpr (EPI == MX_ROWS) {
+            // The rows go to shared memory and from there, 128 columns of a row at a
+            // time, by bulk copies: stored from registers, 32 columns at a time, they
+            // bounded the call (768 x 2048, 49 rows a group, MXFP4 58.7 us, now 33.7;
+            // 15 rows 30.5, now 26.2).
             tmem_ld_wait();
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(args.out) + col0 + lane;
-            const int dl = n0 < 32 ? dest[0] : dest[1];
-            const float wl = n0 < 32 ? w[0] : w[1];
+            const uint32_t dst = out + n0 * OUT_PITCH + 2 * (q * 32 + lane);
+            const float wl = of_row(w, n0);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int d = __shfl_sync(FULL, dl, (n0 & 16) + j);
               const float wj = __shfl_sync(FULL, wl, (n0 & 16) + j);
-              const __nv_bfloat16 v = __float2bfloat16_rn(wj * __uint_as_float(g[j]));
-              if (d >= 0) out[(size_t)d * args.n_valid] = v;
+              st_shared_b16(dst + j * OUT_PITCH,
+                            __bfloat16_as_ushort(__float2bfloat16_rn(wj * __uint_as_float(g[j]))));
             }
           } else {
             uint32_t u[16];
-            tmem_ld_32x32b_x16(tb + CHUNK + n0, u);
+            tmem_ld_32x32b_x16(tb + C + n0, u);
             tmem_ld_wait();
             const int left = col0 < args.n_valid ? t.rows - n0 : 0;  // whole blocks of 32 columns
             const int row = t.row0 + n0;
@@ -448,18 +474,18 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (lane == j) bytes = byte;
               h[j] = byte == 255u ? 0.0f : h[j] * mx_inverse_scale(byte);
             }
-            uint8_t* out = static_cast<uint8_t*>(args.out) +
+            uint8_t* dst = static_cast<uint8_t*>(args.out) +
                            ((size_t)row * args.n_valid + col0) / MxFmt<FMT>::kPerByte;
             const int pitch = args.n_valid / MxFmt<FMT>::kPerByte;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               if constexpr (FMT == MOE_MXFP8) {
                 const uint8_t c = static_cast<uint8_t>(mx_pack_e4m3(h[j], 0.f, 0.f, 0.f));
-                if (j < left) out[(size_t)j * pitch + lane] = c;
+                if (j < left) dst[(size_t)j * pitch + lane] = c;
               } else {
                 const float o = __shfl_xor_sync(FULL, h[j], 1);
                 const uint8_t c = mx_pack_e2m1_pair(h[j], o);
-                if (j < left && (lane & 1) == 0) out[(size_t)j * pitch + (lane >> 1)] = c;
+                if (j < left && (lane & 1) == 0) dst[(size_t)j * pitch + (lane >> 1)] = c;
               }
             }
             // a word's bytes past the last column's block are 0
@@ -471,9 +497,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&st.tempty[acc]);
+        if constexpr (EPI == MX_ROWS) {
+          fence_proxy_async_smem();  // these writes -> the copies
+          four_warps_sync(1);
+          if (dest >= 0)
+            bulk_store(static_cast<__nv_bfloat16*>(args.out) + (size_t)dest * args.n_valid +
+                           t.nt * WM,
+                       out + crow * OUT_PITCH, 2 * min(WM, args.n_valid - t.nt * WM));
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
+      // the last item's copies have left shared memory and are written
+      if constexpr (EPI == MX_ROWS) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
 
@@ -506,17 +543,32 @@ cudaError_t make_tmap_matrices(CUtensorMap* map, const void* base, uint64_t grou
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int FMT, int EPI, bool GATHER = false>
+template <int FMT, int EPI, int C, bool GATHER = false>
 cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& args,
-                   int grid, cudaStream_t stream) {
-  constexpr size_t smem = 1024 + Shape<FMT, EPI>::kOffTail + sizeof(SmemTail);
+                   cudaStream_t stream) {
+  constexpr size_t smem = 1024 + Shape<FMT, EPI, C>::kOffTail + sizeof(SmemTail);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<int> smem_set[MAX_DEVICES];
-  const cudaError_t e =
-      set_smem_limit_per_device(grouped_mx_few_kernel<FMT, EPI, GATHER>, (int)smem, smem_set);
+  auto kernel = grouped_mx_few_kernel<FMT, EPI, C, GATHER>;
+  const cudaError_t e = set_smem_limit_per_device(kernel, (int)smem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_chained(grouped_mx_few_kernel<FMT, EPI, GATHER>, dim3(grid), dim3(THREADS), smem, stream,
-                        tmW, tmX, args);
+  const long long items = ((long long)args.rows / C + args.groups) * args.n_tiles;
+  const int sms = num_sms();
+  return launch_chained(kernel, dim3((unsigned)(items < sms ? items : sms)), dim3(THREADS), smem,
+                        stream, tmW, tmX, args);
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& args,
+                       int epi, bool wide, cudaStream_t stream) {
+  if (args.tok_of)
+    return epi == MX_SWIGLU ? launch<FMT, MX_SWIGLU, 64, true>(tmW, tmX, args, stream)
+                            : cudaErrorInvalidValue;
+  if (epi == MX_SWIGLU)
+    return wide ? launch<FMT, MX_SWIGLU, 96>(tmW, tmX, args, stream)
+                : launch<FMT, MX_SWIGLU, 64>(tmW, tmX, args, stream);
+  return wide ? launch<FMT, MX_ROWS, 128>(tmW, tmX, args, stream)
+              : launch<FMT, MX_ROWS, 64>(tmW, tmX, args, stream);
 }
 
 }  // namespace
@@ -534,20 +586,9 @@ cudaError_t launch_grouped_mx_few(int fmt, int epi, const void* a, const void* b
   args.n_out_tile = WM;
   args.n_tiles = (args.n_valid + WM - 1) / WM;
   args.b_second = args.n_valid;  // MX_SWIGLU: the up rows
-  const long long items = ((long long)args.rows / CHUNK + args.groups) * args.n_tiles;
-  const int sms = num_sms();
-  const int grid = (int)(items < sms ? items : sms);
-  if (args.tok_of) {
-    if (epi != MX_SWIGLU) return cudaErrorInvalidValue;
-    return fmt == MOE_MXFP8
-               ? launch<MOE_MXFP8, MX_SWIGLU, true>(tmW, tmX, args, grid, stream)
-               : launch<MOE_MXFP4, MX_SWIGLU, true>(tmW, tmX, args, grid, stream);
-  }
-  if (fmt == MOE_MXFP8)
-    return epi == MX_SWIGLU ? launch<MOE_MXFP8, MX_SWIGLU>(tmW, tmX, args, grid, stream)
-                            : launch<MOE_MXFP8, MX_ROWS>(tmW, tmX, args, grid, stream);
-  return epi == MX_SWIGLU ? launch<MOE_MXFP4, MX_SWIGLU>(tmW, tmX, args, grid, stream)
-                          : launch<MOE_MXFP4, MX_ROWS>(tmW, tmX, args, grid, stream);
+  const bool wide = args.rows > WIDE_ROWS * (long long)args.groups;
+  return fmt == MOE_MXFP8 ? launch_fmt<MOE_MXFP8>(tmW, tmX, args, epi, wide, stream)
+                          : launch_fmt<MOE_MXFP4>(tmW, tmX, args, epi, wide, stream);
 }
 
 }  // namespace rmoe

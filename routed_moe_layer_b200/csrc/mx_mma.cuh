@@ -194,6 +194,31 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Named barrier of four warps that work together (id 1..15).
+__device__ __forceinline__ void four_warps_sync(int id) {
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
+
+// The same, and whether ok holds in all of them.
+__device__ __forceinline__ bool four_warps_agree(int id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, r;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "bar.red.and.pred r, %1, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}\n"
+      : "=r"(all)
+      : "r"(id), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return all != 0;
+}
+
+// Shared memory to global memory (16-byte aligned, whole 16 bytes), part of this
+// thread's open group of copies.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- host
 inline PFN_cuTensorMapEncodeTiled_v12000 mx_encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
