@@ -692,20 +692,24 @@ MxGemmArgs mx_args(const uint8_t* a_scales, const int32_t* offsets, int32_t R, i
   return g;
 }
 
-// Few rows per group on average: the operands swapped.  128 experts, H = 2048,
-// I = 768, cold L2, swapped against pair tiles.  Up (its output is one byte or
-// less a column): MXFP8 15 rows a group 88.2 / 92.4 us, 64 rows 94.9 / 94.0; MXFP4
-// 49.2 / 53.3, 52.5 / 55.6.  Rows of bf16, whose stores cost the swapped form's
-// four epilogue warps more: MXFP8 15 rows 54.4 / 59.7, 24 rows 59.0 / 61.1, 32 rows
-// 66.6 / 60.8; MXFP4 (whose weights stream in half the time) 15 rows 41.3 / 43.9,
-// 24 rows 48.4 / 44.5.
-bool mx_few(int fmt, int epi, int64_t rows, int64_t groups) {
-  return rows <= (epi == MX_SWIGLU ? 64 : fmt == MOE_MXFP8 ? 24 : 16) * groups;
+// Few rows per group on average: the operands swapped.  128 experts, H = 2048, I =
+// 768, cold L2, swapped against pair tiles.  Up: MXFP8 64 rows a group 90 / 107 us, 96
+// rows 109 / 111, 128 rows 135 / 116; MXFP4 64 rows 50.7 / 57.2, 96 rows 64.4 / 59.0.
+// Down: MXFP8 49 rows 43.0 / 53.7, 128 rows 61.8 / 63.7, 187 rows 80.4 / 73.6; MXFP4
+// 49 rows 29.8 / 38.7, 96 rows 39.8 / 42.1, 128 rows 46.9 / 45.5.
+// Rows of bf16 also where the swapped form's items (128 columns of up to 128 rows) are
+// no more than the SMs, and pair tiles would leave most SMs idle: one group of 1,024
+// rows, K = 2048, N = 1024, MXFP8 10.6 / 12.2, 2 x 512 rows, K = 256, N = 1536, MXFP4
+// 4.7 / 7.3.  (The up product gained nothing there: 2048 x 256 MXFP8 28.0 / 25.0.)
+bool mx_few(int fmt, int epi, int64_t rows, int64_t groups, int64_t n) {
+  if (epi == MX_SWIGLU) return rows <= (fmt == MOE_MXFP8 ? 96 : 80) * groups;
+  return rows <= (fmt == MOE_MXFP8 ? 128 : 112) * groups ||
+         (rows / 128 + groups) * ((n + 127) / 128) <= num_sms();
 }
 
 cudaError_t mx_product(int fmt, int epi, const void* a, const void* b, const MxGemmArgs& g,
                        cudaStream_t s) {
-  return mx_few(fmt, epi, g.rows, g.groups) ? launch_grouped_mx_few(fmt, epi, a, b, g, s)
+  return mx_few(fmt, epi, g.rows, g.groups, g.n_valid) ? launch_grouped_mx_few(fmt, epi, a, b, g, s)
                                   : launch_grouped_mx(fmt, epi, a, b, g, s);
 }
 
@@ -1307,7 +1311,7 @@ int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int3
   dn.row_dest = row_dest;
   dn.out_rows = y_rows;
   dn.out = y;
-  dn.after_up = mx_few(fmt, MX_SWIGLU, R, E) ? 1 : 0;
+  dn.after_up = mx_few(fmt, MX_SWIGLU, R, E, I) ? 1 : 0;
   return cuda_status(mx_product(fmt, MX_ROWS, h, w2_codes, dn, s));
 }
 

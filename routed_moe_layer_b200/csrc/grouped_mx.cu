@@ -200,7 +200,7 @@ __device__ __forceinline__ void load_part(uint32_t tb, int part, uint32_t (&v)[E
 template <int EPI>
 __device__ __forceinline__ bool epilogue_agrees(int q, bool ok) {
   if constexpr (EPI == MX_SWIGLU) return ok;
-  return four_warps_agree(q + 1, ok);
+  return warps_agree<4>(q + 1, ok);
 }
 
 // t: this CTA's part of the tile; out: the tile's rows in shared memory (MX_ROWS).
@@ -223,7 +223,7 @@ __device__ __forceinline__ void store_part(const MxGemmArgs& a, const uint32_t (
       if (dest >= a.out_rows) dest = -1;
     }
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last tile's copies
-    four_warps_sync(q + 1);
+    warps_sync<4>(q + 1);
 #pragma unroll
     for (int k = 0; k < EPI_COLS / 8; ++k) {
       uint32_t pk[4];
@@ -236,7 +236,7 @@ __device__ __forceinline__ void store_part(const MxGemmArgs& a, const uint32_t (
       st_shared_v4(out + r_in_tile * OUT_PITCH + part * (EPI_COLS * 2) + 16 * k, pk);
     }
     fence_proxy_async_smem();  // these writes -> the copies
-    four_warps_sync(q + 1);
+    warps_sync<4>(q + 1);
     if (dest >= 0)
       bulk_store(static_cast<__nv_bfloat16*>(a.out) + (size_t)dest * a.n_valid + t.nt * BN,
                  out + crow * OUT_PITCH, 2 * min(BN, a.n_valid - t.nt * BN));

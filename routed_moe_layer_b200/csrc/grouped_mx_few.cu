@@ -3,12 +3,12 @@
 //
 // With 15 rows an expert a 256-row tile spends its MMA time on padding and its
 // tile's fixed costs on little work, and the weights' stream, which bounds such
-// a call, waits for both.  Here 128 weight rows fill the MMA's M and at most 64
-// rows of a group its N (a multiple of 16), so that an MMA takes a quarter of
-// the time or less; one CTA per SM works alone, with 128 KB of weights in
+// a call, waits for both.  Here 128 weight rows fill the MMA's M and at most C = 64
+// or 128 rows of a group its N (a multiple of 16), so that an MMA takes a quarter
+// or half of the time; one CTA per SM works alone, with 80 to 128 KB of weights in
 // flight and two accumulators.
 //
-// Work item = (chunk of at most 64 rows of one group, 128 weight rows):
+// Work item = (chunk of at most C rows of one group, 128 weight rows):
 //   MX_ROWS    out[dest(r), n0 + l] = bf16( row_w[r] * D[l, r] )
 //   MX_SWIGLU  gate rows i0.. and up rows I + i0.. of the weights in two
 //              accumulators: lane l has gate and up of output column i0 + l; the
@@ -18,12 +18,15 @@
 // tcgen05.cp wants (mx_mma.cuh), 8 words a row at a time, two buffers.
 // Warp roles: warp 0 TMA loads; warp 1 TMEM, scales to TMEM, MMAs; warp 2 the
 // weights' scales (of the gate rows), warp 3 those of the up rows and of the
-// rows; warps 4..7 the epilogue.  Every wait is bounded (common.cuh).
+// rows; warps 4..11 the epilogue.  Every wait is bounded (common.cuh).
 //
-// HBM bounds it: 1,920 rows, K = 1024, N = 1536, MXFP8: 39.7 us for 216 MB (5.4 TB/s,
-// 0.84 of the measured copy; pair tiles 51 us).  1,536 items on 148 SMs are 10.4
-// rounds, done in 11.  Chunks of 32 rows with the shared memory they free in
-// deeper staging, and of 128 rows, measured the same.
+// HBM bounds it: 1,920 rows of 128 groups, K = 1024, N = 1536, MXFP8: 38.4 us for 216
+// MB (5.6 TB/s, 0.87 of the measured copy; pair tiles 51 us); 1,536 items on 148 SMs
+// are 10.4 rounds, done in 11.  6,272 rows, K = 768, N = 2048: MXFP8 43.0 us for 253 MB
+// (5.5 TB/s; pair tiles 53.7), MXFP4 29.8 for 135 MB (4.5 TB/s; 38.7).  More stages than
+// these (8 rows, 5 SwiGLU) measured slower: 64 tokens of 128 experts MXFP8 103.5 us and
+// 108.3 or 109.7, MXFP4 60.0 and 63.0 or 64.5 (the first level cache gets what shared
+// memory leaves).
 #include "mx_mma.cuh"
 
 namespace rmoe {
@@ -31,14 +34,13 @@ namespace rmoe {
 namespace {
 
 constexpr int WM = 128;           // weight rows per item (the MMA's M)
-constexpr long long WIDE_ROWS = 32;
 constexpr int KB = 128;           // bytes of a row per K step
 constexpr int XBOX = 32;          // rows per TMA box
 constexpr int W_BYTES = WM * KB;
 constexpr int OUT_PITCH = 2 * WM; // bytes of an output row in shared memory
-constexpr int THREADS = 256;
+constexpr int THREADS = 384;
 constexpr int EPI_WARP0 = 4;
-constexpr int EPI_WARPS = 4;
+constexpr int EPI_WARPS = 8;      // two for each 32 columns, 16 rows in turn
 constexpr int SF_WORDS = 8;       // words per row in a buffer of scales
 constexpr int MAX_STAGES = 6;
 constexpr uint32_t TMEM_COLS = 512;
@@ -401,9 +403,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     } else {
-      // ------------------------------------------------ epilogue warps 4..7
+      // ------------------------------------------------ epilogue warps 4..11
       if (early) pdl_wait();
-      const int q = warp & 3;
+      const int q = warp & 3, part = (warp - EPI_WARP0) >> 2;
       constexpr int COPIES = C / EPI_WARPS;  // MX_ROWS: rows that a warp copies, one a lane
       const uint32_t out = smem0 + S::kOffOut;
       int acc = 0;
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
         const Tile t = walk.tile(mts, rs);
         const int col0 = t.nt * WM + q * 32;  // the warp's first output column
-        const int crow = q * COPIES + lane;   // MX_ROWS: this lane's row of the copies,
+        const int crow = (warp - EPI_WARP0) * COPIES + lane;   // MX_ROWS: this lane's row of the copies,
         int dest = -1;                        // its output row (-1: none),
         float w[C / 32];                      // and the weights of rows l, l + 32, ..
         if constexpr (EPI == MX_ROWS) {
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = __all_sync(FULL, mbar_wait(&st.tfull[acc], acc_phase, wc, 76));
         if constexpr (EPI == MX_ROWS) {
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last item's copies
-          ok = four_warps_agree(1, ok);
+          ok = warps_agree<EPI_WARPS>(1, ok);
         }
         if (!ok) break;
         tc_fence_after_sync();
@@ -439,14 +441,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         // reductions and stores overlap (row by row they cost 170 cycles each,
         // and bounded the call from 8 rows a group on)
 #pragma unroll 1
-        for (int n0 = 0; n0 < t.rows; n0 += 16) {
+        for (int n0 = 16 * part; n0 < t.rows; n0 += 32) {
           uint32_t g[16];
           tmem_ld_32x32b_x16(tb + n0, g);
           if constexpr (EPI == MX_ROWS) {
             // The rows go to shared memory and from there, 128 columns of a row at a
             // time, by bulk copies: stored from registers, 32 columns at a time, they
-            // bounded the call (768 x 2048, 49 rows a group, MXFP4 58.7 us, now 33.7;
-            // 15 rows 30.5, now 26.2).
+            // bounded the call (768 x 2048, 49 rows a group, MXFP4, items of 64 rows: 58.7
+            // us, now 32.1; 15 rows 30.5, now 25.4).  Eight warps: four took 33.4, and
+            // 36.4 instead of 29.8 with items of 128 rows.
             tmem_ld_wait();
             const uint32_t dst = out + n0 * OUT_PITCH + 2 * (q * 32 + lane);
             const float wl = of_row(w, n0);
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&st.tempty[acc]);
         if constexpr (EPI == MX_ROWS) {
           fence_proxy_async_smem();  // these writes -> the copies
-          four_warps_sync(1);
+          warps_sync<EPI_WARPS>(1);
           if (dest >= 0)
             bulk_store(static_cast<__nv_bfloat16*>(args.out) + (size_t)dest * args.n_valid +
                            t.nt * WM,
@@ -558,17 +561,24 @@ cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmA
                         stream, tmW, tmX, args);
 }
 
+// MX_ROWS: rows per group, on average, from which items hold up to 128 rows and not
+// 64 (groups are uneven: fewer read their weights twice).  128 experts, K = 768, N =
+// 2048, 64 / 128 rows an item: MXFP8 15 rows a group 38.0 / 38.8 us, 32 rows 41.5 /
+// 40.2, 49 rows 48.9 / 43.0; MXFP4 25.4 / 25.4, 27.5 / 27.2, 32.1 / 29.8.  The up
+// product, with two accumulators a row, has room for 96 rows, which measured within
+// 5% of 64 either way.
+constexpr long long WIDE_ROWS = 24;
+
 template <int FMT>
 cudaError_t launch_fmt(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& args,
-                       int epi, bool wide, cudaStream_t stream) {
+                       int epi, cudaStream_t stream) {
   if (args.tok_of)
     return epi == MX_SWIGLU ? launch<FMT, MX_SWIGLU, 64, true>(tmW, tmX, args, stream)
                             : cudaErrorInvalidValue;
-  if (epi == MX_SWIGLU)
-    return wide ? launch<FMT, MX_SWIGLU, 96>(tmW, tmX, args, stream)
-                : launch<FMT, MX_SWIGLU, 64>(tmW, tmX, args, stream);
-  return wide ? launch<FMT, MX_ROWS, 128>(tmW, tmX, args, stream)
-              : launch<FMT, MX_ROWS, 64>(tmW, tmX, args, stream);
+  if (epi == MX_SWIGLU) return launch<FMT, MX_SWIGLU, 64>(tmW, tmX, args, stream);
+  return args.rows > WIDE_ROWS * args.groups
+             ? launch<FMT, MX_ROWS, 128>(tmW, tmX, args, stream)
+             : launch<FMT, MX_ROWS, 64>(tmW, tmX, args, stream);
 }
 
 }  // namespace
@@ -586,9 +596,8 @@ cudaError_t launch_grouped_mx_few(int fmt, int epi, const void* a, const void* b
   args.n_out_tile = WM;
   args.n_tiles = (args.n_valid + WM - 1) / WM;
   args.b_second = args.n_valid;  // MX_SWIGLU: the up rows
-  const bool wide = args.rows > WIDE_ROWS * (long long)args.groups;
-  return fmt == MOE_MXFP8 ? launch_fmt<MOE_MXFP8>(tmW, tmX, args, epi, wide, stream)
-                          : launch_fmt<MOE_MXFP4>(tmW, tmX, args, epi, wide, stream);
+  return fmt == MOE_MXFP8 ? launch_fmt<MOE_MXFP8>(tmW, tmX, args, epi, stream)
+                          : launch_fmt<MOE_MXFP4>(tmW, tmX, args, epi, stream);
 }
 
 }  // namespace rmoe

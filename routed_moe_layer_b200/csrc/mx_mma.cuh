@@ -194,19 +194,21 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Named barrier of four warps that work together (id 1..15).
-__device__ __forceinline__ void four_warps_sync(int id) {
-  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+// Named barrier of N warps that work together (id 1..15).
+template <int N>
+__device__ __forceinline__ void warps_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(32 * N) : "memory");
 }
 
 // The same, and whether ok holds in all of them.
-__device__ __forceinline__ bool four_warps_agree(int id, bool ok) {
+template <int N>
+__device__ __forceinline__ bool warps_agree(int id, bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, r;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-      "bar.red.and.pred r, %1, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}\n"
+      "bar.red.and.pred r, %1, %3, p;\n\tselp.u32 %0, 1, 0, r;\n\t}\n"
       : "=r"(all)
-      : "r"(id), "r"(static_cast<uint32_t>(ok))
+      : "r"(id), "r"(static_cast<uint32_t>(ok)), "n"(32 * N)
       : "memory");
   return all != 0;
 }

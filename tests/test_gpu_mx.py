@@ -227,7 +227,7 @@ def test_add_rmsnorm_propagates_nan_to_its_row_alone():
 
 
 # ------------------------------------------------------------------ products
-SHAPES = [  # R, E, N, K; up to 64 rows an expert on average the operands are swapped
+SHAPES = [  # R, E, N, K: swapped operands, items of 64 and of 128 rows (bf16: pair tiles too)
     (1, 1, 32, 32), (8, 16, 64, 96), (40, 3, 96, 160), (257, 5, 160, 352), (300, 2, 544, 512),
     (600, 1, 256, 128), (1000, 7, 288, 1056), (515, 128, 64, 256), (65, 1, 32, 32),
     (130, 2, 128, 2112), (128, 2, 128, 2112), (64, 1, 416, 1184), (200, 4, 64, 64),
@@ -313,7 +313,7 @@ def test_every_element_and_scale_reaches_the_product(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("R", [24, 96])  # swapped operands, pair tiles
+@pytest.mark.parametrize("R", [24, 96])
 def test_powers_far_from_each_other(R, fmt):
     """Blocks of rows with powers from 2^-126 to 2^120 against columns with the
     opposite ones: each product lies near 1 and is exact, however far its
@@ -404,6 +404,98 @@ def test_bad_offsets_are_reported_and_write_nothing_outside():
     assert (buf[:R] == K).all()
 
 
+# R, E, N, K of pair tiles: over 128 rows an expert, and more items of 128 x 128 than SMs
+PAIR_SHAPES = [(1000, 1, 2720, 352), (1500, 5, 1312, 1056), (3000, 3, 800, 96), (5600, 40, 416, 32),
+               (1100, 1, 2560, 2112), (700, 1, 3200, 160)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R,E,N,K", PAIR_SHAPES)
+def test_grouped_mm_mx_pair_tiles(R, E, N, K, fmt):
+    assert R > 128 * E and (R // 128 + E) * -(-N // 128) > 148
+    xc, xs, x = operands(R, K, fmt, R + K)
+    wc, wsc, w = operands(N, K, fmt, N + K, lead=E, scale=0.1)
+    lead, tail = 2, 3
+    off = groups(R, E, R, lead, tail)
+    offd = torch.from_numpy(off).to(DEV)
+    ws = ops.alloc_workspace(256, DEV)
+    out = torch.full((R, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = ops.grouped_mm_mx(xc, xs, wc, wsc, offd, fmt, out=out, workspace=ws)
+    assert ops.read_device_status(ws)[0] == 0
+    check_product(y, x, w, off)
+    assert (y[:lead] == 7).all() and (y[R - tail:] == 7).all()
+    # weights that scale exactly, destinations in any order, two of them nowhere
+    g = gen(9)
+    row_w = 2.0 ** torch.randint(-2, 3, (R,), generator=g).float()
+    dest = torch.randperm(R + 50, generator=g)[:R].int()
+    dest[10], dest[20] = -1, R + 50
+    z = torch.full((R + 50, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ops.grouped_mm_mx(xc, xs, wc, wsc, offd, fmt, row_w=row_w.to(DEV), row_dest=dest.to(DEV), out=z)
+    kept = torch.ones(R, dtype=torch.bool)
+    kept[[10, 20]] = False
+    kept[:lead] = False
+    kept[R - tail:] = False
+    want = (y.float() * row_w.to(DEV)[:, None]).bfloat16()
+    assert torch.equal(z[dest[kept].long().to(DEV)], want[kept.to(DEV)])
+    free = np.setdiff1d(np.arange(R + 50), dest.numpy()[kept.numpy()])
+    assert (z[torch.from_numpy(free).to(DEV)] == 7).all()
+    # the bits of the swapped form
+    lo, hi = int(off[0]), min(int(off[1]), int(off[0]) + 50)
+    part = torch.full((E + 1,), hi - lo, dtype=torch.int32, device=DEV)
+    part[0] = 0
+    a = ops.grouped_mm_mx(xc[lo:hi].contiguous(), xs[:, lo:hi].contiguous(), wc, wsc, part, fmt)
+    assert torch.equal(a, y[lo:hi])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_pair_tiles_read_every_element_and_scale(fmt):
+    """As test_every_element_and_scale_reaches_the_product; a NaN block of a row and one
+    of a column besides."""
+    K, N = 512, 3840
+    grid = mx.mx_grid(fmt)
+    n = 2 * len(grid)
+    signed = np.array([c if c < len(grid) else c - len(grid) + (128 if fmt == "mxfp8" else 8)
+                       for c in range(n)], np.uint8)
+    rng = np.random.default_rng(3)
+    wc = signed[rng.integers(0, n, (N, K))]
+    wsb = rng.integers(117, 137, (N, K // 32)).astype(np.uint8)
+    xc = np.zeros((K, K), np.uint8)
+    xc[np.arange(K), np.arange(K)] = 0x38 if fmt == "mxfp8" else 2  # 1.0
+    xsb = rng.integers(117, 137, (K, K // 32)).astype(np.uint8)
+    ref = mx.mx_values(xc, xsb, fmt) @ mx.mx_values(wc, wsb, fmt).T  # one term each: exact
+    off = torch.tensor([0, K], dtype=torch.int32, device=DEV)
+
+    def product():
+        xd, xsd = stored(xc, xsb, fmt)
+        wd, wsd = stored(wc, wsb, fmt)
+        return ops.grouped_mm_mx(xd.to(DEV), xsd.to(DEV), wd[None].to(DEV), wsd[None].to(DEV), off, fmt)
+    assert np.array_equal(to_np(product()), ref)
+    xsb[300, 7] = 255
+    wsb[2000, 3] = 255
+    got = to_np(product())
+    ref[300] = np.nan
+    ref[:, 2000] = np.nan
+    assert np.array_equal(got, ref, equal_nan=True)
+
+
+def test_pair_tiles_bad_offsets():
+    R, E, N, K = 2000, 4, 1280, 64
+    x = torch.ones(R, K, dtype=torch.bfloat16, device=DEV)
+    xc, xs = ops.mx_quantize(x, "mxfp4")
+    wc, wsc = ops.mx_quantize(torch.ones(E, N, K, dtype=torch.bfloat16, device=DEV), "mxfp4")
+    buf = torch.full((R + 64, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = ops.alloc_workspace(256, DEV)
+    for bad in ([0, 100, 300, 500, R + 50], [-5, 10, 20, 30, 40], [0, 400, 200, 500, 600],
+                [2 ** 30, 2 ** 31 - 1, 5, 6, 7]):
+        off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        ops.grouped_mm_mx(xc, xs, wc, wsc, off, "mxfp4", out=buf[:R], workspace=ws)
+        assert ops.read_device_status(ws)[0] == 6
+        assert (buf[R:] == 7).all()
+    ok = torch.tensor([0, 100, 100, 1900, R], dtype=torch.int32, device=DEV)
+    ops.grouped_mm_mx(xc, xs, wc, wsc, ok, "mxfp4", out=buf[:R], workspace=ws)
+    assert ops.read_device_status(ws)[0] == 0 and (buf[:R] == K).all()
+
+
 # ------------------------------------------------------------------ experts
 def experts_tolerance(x, w13, w2, off, fmt, row_w):
     """ref and the bound of |y - ref|: h's fp32 errors move an element over a
@@ -492,6 +584,29 @@ def test_a_rows_bits_do_not_depend_on_the_other_rows(fmt):
         part = call(lo, mid, hi)
         for a, b in zip(part, full):
             assert torch.equal(a, b[lo:hi])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R,E", [(200, 2), (380, 4), (1400, 2)])
+def test_expert_rows_mx_between_the_forms(R, E, fmt):
+    """Rows on either side of where the up and the down product change their form (1,400
+    rows: both pair tiles): the bits of calls of at most 30 rows."""
+    H, I = 1664, 64
+    xc, xs, _ = operands(R, H, fmt, 1)
+    w13c, w13s, _ = operands(2 * I, H, fmt, 2, lead=E, scale=H ** -0.5)
+    w2c, w2s, _ = operands(H, I, fmt, 3, lead=E, scale=I ** -0.5)
+    off = groups(R, E, 3)
+    tok = torch.randperm(R, generator=gen(2)).int().to(DEV)
+    row_w = torch.rand(R, generator=gen(3)).to(DEV)
+    y = ops.expert_rows_mx(xc, xs, torch.from_numpy(off).to(DEV), w13c, w13s, w2c, w2s, None, fmt,
+                           row_w=row_w, tok_of=tok)
+    for e in range(E):
+        for lo in range(int(off[e]), int(off[e + 1]), 90):
+            hi = min(lo + 30, int(off[e + 1]))
+            part = torch.tensor([0] * (e + 1) + [hi - lo] * (E - e), dtype=torch.int32, device=DEV)
+            a = ops.expert_rows_mx(xc, xs, part, w13c, w13s, w2c, w2s, None, fmt,
+                                   row_w=row_w[lo:hi].contiguous(), tok_of=tok[lo:hi].contiguous())
+            assert torch.equal(a, y[lo:hi])
 
 
 def test_expert_rows_mx_token_outside_counts_as_zeros():
