@@ -279,9 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   constexpr int STAGES = S::kStages;
   pdl_launch_dependents();
   pdl_wait();
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   SmemTail& st = *reinterpret_cast<SmemTail*>(smem + S::kOffTail);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -586,7 +584,7 @@ cudaError_t make_tmap_sb(CUtensorMap* map, const void* base, uint64_t word_rows,
 template <int FMT, int EPI>
 cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSB,
                    const MxGemmArgs& args, int grid, cudaStream_t stream) {
-  constexpr size_t smem = 1024 + Shape<FMT, EPI>::kOffTail + sizeof(SmemTail);
+  constexpr size_t smem = Shape<FMT, EPI>::kOffTail + sizeof(SmemTail);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<int> smem_set[MAX_DEVICES];
   const cudaError_t e =

@@ -22,7 +22,7 @@
 //
 // HBM bounds it: 1,920 rows of 128 groups, K = 1024, N = 1536, MXFP8: 38.4 us for 216
 // MB (5.6 TB/s, 0.87 of the measured copy; pair tiles 51 us); 1,536 items on 148 SMs
-// are 10.4 rounds, done in 11.  6,272 rows, K = 768, N = 2048: MXFP8 43.0 us for 253 MB
+// are 10.4 rounds, done in 11.  6,272 rows, K = 768, N = 2048: MXFP8 43.0 us for 238 MB
 // (5.5 TB/s; pair tiles 53.7), MXFP4 29.8 for 135 MB (4.5 TB/s; 38.7).  More stages than
 // these (8 rows, 5 SwiGLU) measured slower: 64 tokens of 128 experts MXFP8 103.5 us and
 // 108.3 or 109.7, MXFP4 60.0 and 63.0 or 64.5 (the first level cache gets what shared
@@ -42,7 +42,7 @@ constexpr int THREADS = 384;
 constexpr int EPI_WARP0 = 4;
 constexpr int EPI_WARPS = 8;      // two for each 32 columns, 16 rows in turn
 constexpr int SF_WORDS = 8;       // words per row in a buffer of scales
-constexpr int MAX_STAGES = 6;
+constexpr int MAX_STAGES = 5;
 constexpr uint32_t TMEM_COLS = 512;
 
 // C: rows per item at most (the MMA's N, padded to 16).
@@ -51,16 +51,18 @@ struct Shape {
   static constexpr int kWords = FMT == MOE_MXFP8 ? 1 : 2;  // scale words per row and K step
   static constexpr int kTiles = EPI == MX_SWIGLU ? 2 : 1;  // weight tiles per item
   static constexpr int kXBytes = C * KB;
-  static constexpr int kStageBytes = kTiles * W_BYTES + kXBytes;
-  static constexpr int kStages = EPI == MX_SWIGLU ? 4 : C == 64 ? 6 : 5;
+  static constexpr int kStepBytes = kTiles * W_BYTES + kXBytes;
+  static constexpr int kSub = C == 64 ? 2 : 1;  // K steps per stage
+  static constexpr int kStageBytes = kSub * kStepBytes;
+  static constexpr int kStages = EPI == MX_SWIGLU ? 2 : C == 128 ? 5 : FMT == MOE_MXFP8 ? 4 : 3;
   static constexpr uint32_t kAcc = kTiles * C;   // TMEM columns of an accumulator (gate, up)
-  static constexpr uint32_t kTmemSf = 2 * kAcc;  // + 32 per stage: 4 per word of each tile, rows first
+  static constexpr uint32_t kTmemSf = 2 * kAcc;  // + 32 per step: 4 per word of each tile, rows first
   static constexpr int kSfBytes = SF_WORDS * MX_SF_BYTES;  // per operand tile and buffer
   static constexpr int kSfBuf = (kTiles + 1) * kSfBytes;   // the rows', then the weights'
   static constexpr int kOffSf = kStages * kStageBytes;
   static constexpr int kOffOut = kOffSf + 2 * kSfBuf;
   static constexpr int kOffTail = kOffOut + (EPI == MX_ROWS ? C * OUT_PITCH : 0);
-  static_assert(kStages <= MAX_STAGES && kTmemSf + 32 * kStages <= TMEM_COLS, "TMEM");
+  static_assert(kStages <= MAX_STAGES && kTmemSf + 32 * kSub * kStages <= TMEM_COLS, "TMEM");
 };
 
 struct __align__(8) SmemTail {
@@ -160,9 +162,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     grouped_mx_few_kernel(const __grid_constant__ CUtensorMap tmW,
                           const __grid_constant__ CUtensorMap tmX, const MxGemmArgs args) {
   using S = Shape<FMT, EPI, C>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  constexpr int SUB = S::kSub;
+  extern __shared__ __align__(1024) uint8_t smem[];
   SmemTail& st = *reinterpret_cast<SmemTail*>(smem + S::kOffTail);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -228,30 +229,37 @@ __global__ void __launch_bounds__(THREADS, 1)
         if constexpr (GATHER) item_tokens(args, t, lane, tok);
         auto load_weights = [&](int st_i, int ks) {  // one lane
           uint8_t* sw = smem + (size_t)st_i * S::kStageBytes + S::kXBytes;
-          mbar_arrive_expect_tx(&st.full[st_i], tx);
+          const int n = min(SUB, k_steps - ks);
+          mbar_arrive_expect_tx(&st.full[st_i], n * tx);
 #pragma unroll
-          for (int w = 0; w < S::kTiles; ++w)
-            tma_load_3d(sw + w * W_BYTES, &tmW, &st.full[st_i], ks * KB,
-                        w_row + w * args.b_second, t.g);
+          for (int u = 0; u < SUB; ++u)
+            if (u < n)
+#pragma unroll
+              for (int w = 0; w < S::kTiles; ++w)
+                tma_load_3d(sw + u * S::kStepBytes + w * W_BYTES, &tmW, &st.full[st_i],
+                            (ks + u) * KB, w_row + w * args.b_second, t.g);
         };
         if (early && item == first) {
-          ahead = min(S::kStages, k_steps);
+          ahead = min(S::kStages, (k_steps + SUB - 1) / SUB);
           if (elect_one())
-            for (int ks = 0; ks < ahead; ++ks) load_weights(ks, ks);
+            for (int s = 0; s < ahead; ++s) load_weights(s, s * SUB);
           __syncwarp();
           pdl_wait();
         }
-        for (int ks = 0; ks < k_steps; ++ks) {
+        for (int ks = 0; ks < k_steps; ks += SUB) {
           if (!__all_sync(FULL, mbar_wait(&st.empty[stage], phase ^ 1u, wc, 71))) {
             ok = false;
             break;
           }
           uint8_t* sx = smem + (size_t)stage * S::kStageBytes;
+          const int steps = min(SUB, k_steps - ks);
           if (elect_one()) {
             if (ahead == 0) load_weights(stage, ks);
             if constexpr (!GATHER)
-              for (int b = 0; b < nb; ++b)
-                tma_load_2d(sx + b * XBOX * KB, &tmX, &st.full[stage], ks * KB, t.row0 + b * XBOX);
+              for (int u = 0; u < steps; ++u)
+                for (int b = 0; b < nb; ++b)
+                  tma_load_2d(sx + u * S::kStepBytes + b * XBOX * KB, &tmX, &st.full[stage],
+                              (ks + u) * KB, t.row0 + b * XBOX);
           }
           if (ahead > 0) --ahead;
           if constexpr (GATHER) {
@@ -260,7 +268,9 @@ __global__ void __launch_bounds__(THREADS, 1)
               const int r = __shfl_sync(FULL, of_row(tok, n), n & 31);
               // a row past the last one reads zeros
               if (lead)
-                tma_load_2d(sx + n * KB, &tmX, &st.full[stage], ks * KB, r < 0 ? args.a_rows : r);
+                for (int u = 0; u < steps; ++u)
+                  tma_load_2d(sx + u * S::kStepBytes + n * KB, &tmX, &st.full[stage],
+                              (ks + u) * KB, r < 0 ? args.a_rows : r);
             }
           }
           armed |= 1u << stage;
@@ -283,7 +293,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
       bool ok = true;
       const uint64_t dx0 = sdesc_kmajor_sw128(smem0), dsf0 = sdesc_rows16(sf0);
-      const int last = args.k_bytes - (k_steps - 1) * KB;  // bytes of a row in the last step
       for (int item = first; ok && item < total; item += step) {
         if (item != first) walk.next(dm, dn, args.n_tiles, args.groups, mts);
         const Tile t = walk.tile(mts, rs);
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t d = tmem_base + acc * S::kAcc;
         int chunk_left = 0;
         uint64_t dsf = dsf0;
-        for (int ks = 0; ks < k_steps; ++ks) {
+        for (int ks = 0; ks < k_steps; ks += SUB) {
           if (chunk_left == 0) {
             if (!__all_sync(FULL, mbar_wait(&st.sf_full[buf], sf_phase, wc, 72))) {
               ok = false;
@@ -305,17 +314,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             break;
           }
           tc_fence_after_sync();
-          --chunk_left;
-          const bool chunk_done = chunk_left == 0 || ks + 1 == k_steps;
-          const uint32_t sf = tmem_base + S::kTmemSf + 32 * stage;
-          const uint64_t dx = dx0 + static_cast<uint64_t>(stage * (S::kStageBytes >> 4));
+          chunk_left -= SUB;
+          const bool chunk_done = chunk_left == 0 || ks + SUB >= k_steps;
+          const uint32_t sf0 = tmem_base + S::kTmemSf + 32 * SUB * stage;
+          const uint64_t dx0s = dx0 + static_cast<uint64_t>(stage * (S::kStageBytes >> 4));
           if (elect_one()) {
 #pragma unroll
-            for (int o = 0; o < S::kTiles + 1; ++o)
+            for (int u = 0; u < SUB; ++u)  // (past the last step: words that nothing uses)
 #pragma unroll
-              for (int w = 0; w < S::kWords; ++w)
-                tmem_copy_sf(sf + 4 * (S::kWords * o + w),
-                             dsf + ((o * S::kSfBytes + w * MX_SF_BYTES) >> 4));
+              for (int o = 0; o < S::kTiles + 1; ++o)
+#pragma unroll
+                for (int w = 0; w < S::kWords; ++w)
+                  tmem_copy_sf(sf0 + 32 * u + 4 * (S::kWords * o + w),
+                               dsf + ((o * S::kSfBytes + (u * S::kWords + w) * MX_SF_BYTES) >> 4));
           }
           if (ks == 0) {
             if (!__all_sync(FULL, mbar_wait(&st.tempty[acc], acc_phase ^ 1u, wc, 74))) {
@@ -326,22 +337,29 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           if (elect_one()) {
             // 32 bytes of every row per MMA; the scale word, and the byte in it
+            auto mma = [&](int u, int kk) {
+              const uint64_t dx = dx0s + u * (S::kStepBytes >> 4);
+              const uint32_t sf = sf0 + 32 * u, word = 4 * (kk * S::kWords / 4);
+              const uint32_t id = idesc_sf(idesc, FMT == MOE_MXFP8 ? kk : 2 * (kk & 1));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (ks + 1 < k_steps || kk * 32 < last) {
-                const uint32_t word = 4 * (kk * S::kWords / 4);
-                const uint32_t id = idesc_sf(idesc, FMT == MOE_MXFP8 ? kk : 2 * (kk & 1));
+              for (int w = 0; w < S::kTiles; ++w)
+                umma_mx<FMT>(d + w * C, dx + ((S::kXBytes + w * W_BYTES) >> 4) + 2 * kk,
+                             dx + 2 * kk, id, sf + 4 * S::kWords * (1 + w) + word, sf + word,
+                             (ks | u | kk) != 0 ? 1u : 0u);
+            };
+            if (ks + SUB < k_steps) {
 #pragma unroll
-                for (int w = 0; w < S::kTiles; ++w)
-                  umma_mx<FMT>(d + w * C, dx + ((S::kXBytes + w * W_BYTES) >> 4) + 2 * kk,
-                               dx + 2 * kk, id, sf + 4 * S::kWords * (1 + w) + word, sf + word,
-                               (ks | kk) != 0 ? 1u : 0u);
-              }
+              for (int m = 0; m < 4 * SUB; ++m) mma(m >> 2, m & 3);
+            } else {
+#pragma unroll
+              for (int m = 0; m < 4 * SUB; ++m)
+                if (ks * KB + m * 32 < args.k_bytes) mma(m >> 2, m & 3);
+            }
             umma_commit(&st.empty[stage]);
             if (chunk_done) umma_commit(&st.sf_empty[buf]);
-            if (ks + 1 == k_steps) umma_commit(&st.tfull[acc]);
+            if (ks + SUB >= k_steps) umma_commit(&st.tfull[acc]);
           }
-          dsf += S::kWords * (MX_SF_BYTES >> 4);
+          dsf += SUB * S::kWords * (MX_SF_BYTES >> 4);
           if (chunk_done) {
             chunk_left = 0;
             buf ^= 1;
@@ -549,7 +567,7 @@ cudaError_t make_tmap_matrices(CUtensorMap* map, const void* base, uint64_t grou
 template <int FMT, int EPI, int C, bool GATHER = false>
 cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& args,
                    cudaStream_t stream) {
-  constexpr size_t smem = 1024 + Shape<FMT, EPI, C>::kOffTail + sizeof(SmemTail);
+  constexpr size_t smem = Shape<FMT, EPI, C>::kOffTail + sizeof(SmemTail);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<int> smem_set[MAX_DEVICES];
   auto kernel = grouped_mx_few_kernel<FMT, EPI, C, GATHER>;
