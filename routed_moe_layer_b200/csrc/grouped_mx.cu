@@ -607,31 +607,26 @@ __global__ void __launch_bounds__(256)
                      uint4* __restrict__ codes_out, uint32_t* __restrict__ scales_out) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ int tok[GATHER_ROWS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = blockIdx.x * GATHER_ROWS;
   const int rows = min(GATHER_ROWS, R - row0);
-  if (threadIdx.x < GATHER_ROWS) {
-    const int t = (int)threadIdx.x < rows ? tok_of[row0 + threadIdx.x] : -1;
-    tok[threadIdx.x] = t >= 0 && t < T ? t : -1;
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int c = lane; c < vecs; c += 32) {
+  int mine = lane < rows ? tok_of[row0 + lane] : -1;  // the token of row lane
+  if (mine >= T) mine = -1;
+  for (int c0 = 0; c0 < vecs; c0 += 32) {
+    const int c = c0 + lane;
     uint4 v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int t = tok[warp * 4 + j];
-      v[j] = t >= 0 ? codes[(size_t)t * vecs + c] : make_uint4(0, 0, 0, 0);
+      const int t = __shfl_sync(FULL, mine, warp * 4 + j);
+      v[j] = t >= 0 && c < vecs ? codes[(size_t)t * vecs + c] : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (warp * 4 + j < rows) codes_out[(size_t)(row0 + warp * 4 + j) * vecs + c] = v[j];
+      if (warp * 4 + j < rows && c < vecs) codes_out[(size_t)(row0 + warp * 4 + j) * vecs + c] = v[j];
   }
   for (int w = warp; w < words; w += 8)
-    if (lane < rows) {
-      const int t = tok[lane];
-      scales_out[(size_t)w * R + row0 + lane] = t >= 0 ? scales[(size_t)w * T + t] : 0u;
-    }
+    if (lane < rows)
+      scales_out[(size_t)w * R + row0 + lane] = mine >= 0 ? scales[(size_t)w * T + mine] : 0u;
 }
 
 }  // namespace

@@ -46,7 +46,7 @@ constexpr int MAX_STAGES = 5;
 constexpr uint32_t TMEM_COLS = 512;
 
 // C: rows per item at most (the MMA's N, padded to 16).
-template <int FMT, int EPI, int C>
+template <int FMT, int EPI, int C, int STAGES>
 struct Shape {
   static constexpr int kWords = FMT == MOE_MXFP8 ? 1 : 2;  // scale words per row and K step
   static constexpr int kTiles = EPI == MX_SWIGLU ? 2 : 1;  // weight tiles per item
@@ -54,7 +54,7 @@ struct Shape {
   static constexpr int kStepBytes = kTiles * W_BYTES + kXBytes;
   static constexpr int kSub = C == 64 ? 2 : 1;  // K steps per stage
   static constexpr int kStageBytes = kSub * kStepBytes;
-  static constexpr int kStages = EPI == MX_SWIGLU ? 2 : C == 128 ? 5 : FMT == MOE_MXFP8 ? 4 : 3;
+  static constexpr int kStages = STAGES;
   static constexpr uint32_t kAcc = kTiles * C;   // TMEM columns of an accumulator (gate, up)
   static constexpr uint32_t kTmemSf = 2 * kAcc;  // + 32 per step: 4 per word of each tile, rows first
   static constexpr int kSfBytes = SF_WORDS * MX_SF_BYTES;  // per operand tile and buffer
@@ -157,11 +157,11 @@ __device__ __forceinline__ V of_row(const V (&v)[J], int n) {
 }
 
 // GATHER: row r of the groups is row tok_of[r] of X, loaded by a TMA box of its own.
-template <int FMT, int EPI, int C, bool GATHER>
+template <int FMT, int EPI, int C, int STAGES, bool GATHER>
 __global__ void __launch_bounds__(THREADS, 1)
     grouped_mx_few_kernel(const __grid_constant__ CUtensorMap tmW,
                           const __grid_constant__ CUtensorMap tmX, const MxGemmArgs args) {
-  using S = Shape<FMT, EPI, C>;
+  using S = Shape<FMT, EPI, C, STAGES>;
   constexpr int SUB = S::kSub;
   extern __shared__ __align__(1024) uint8_t smem[];
   SmemTail& st = *reinterpret_cast<SmemTail*>(smem + S::kOffTail);
@@ -564,13 +564,13 @@ cudaError_t make_tmap_matrices(CUtensorMap* map, const void* base, uint64_t grou
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int FMT, int EPI, int C, bool GATHER = false>
+template <int FMT, int EPI, int C, int STAGES, bool GATHER = false>
 cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& args,
                    cudaStream_t stream) {
-  constexpr size_t smem = Shape<FMT, EPI, C>::kOffTail + sizeof(SmemTail);
+  constexpr size_t smem = Shape<FMT, EPI, C, STAGES>::kOffTail + sizeof(SmemTail);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<int> smem_set[MAX_DEVICES];
-  auto kernel = grouped_mx_few_kernel<FMT, EPI, C, GATHER>;
+  auto kernel = grouped_mx_few_kernel<FMT, EPI, C, STAGES, GATHER>;
   const cudaError_t e = set_smem_limit_per_device(kernel, (int)smem, smem_set);
   if (e != cudaSuccess) return e;
   const long long items = ((long long)args.rows / C + args.groups) * args.n_tiles;
@@ -587,16 +587,22 @@ cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmA
 // 5% of 64 either way.
 constexpr long long WIDE_ROWS = 24;
 
+// Bytes of a row above which items of 64 rows get a fourth stage: MXFP8 K = 2048, N =
+// 1536, 15 rows a group 66.6 us, with three 69.2; K = 768, N = 2048 36.0, with three 35.2;
+// 1,024 bytes the same.
+constexpr int DEEP_BYTES = 1024;
+
 template <int FMT>
 cudaError_t launch_fmt(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& args,
                        int epi, cudaStream_t stream) {
   if (args.tok_of)
-    return epi == MX_SWIGLU ? launch<FMT, MX_SWIGLU, 64, true>(tmW, tmX, args, stream)
+    return epi == MX_SWIGLU ? launch<FMT, MX_SWIGLU, 64, 2, true>(tmW, tmX, args, stream)
                             : cudaErrorInvalidValue;
-  if (epi == MX_SWIGLU) return launch<FMT, MX_SWIGLU, 64>(tmW, tmX, args, stream);
-  return args.rows > WIDE_ROWS * args.groups
-             ? launch<FMT, MX_ROWS, 128>(tmW, tmX, args, stream)
-             : launch<FMT, MX_ROWS, 64>(tmW, tmX, args, stream);
+  if (epi == MX_SWIGLU) return launch<FMT, MX_SWIGLU, 64, 2>(tmW, tmX, args, stream);
+  if (args.rows > WIDE_ROWS * args.groups)
+    return launch<FMT, MX_ROWS, 128, 5>(tmW, tmX, args, stream);
+  return args.k_bytes > DEEP_BYTES ? launch<FMT, MX_ROWS, 64, 4>(tmW, tmX, args, stream)
+                                   : launch<FMT, MX_ROWS, 64, 3>(tmW, tmX, args, stream);
 }
 
 }  // namespace
