@@ -693,17 +693,18 @@ MxGemmArgs mx_args(const uint8_t* a_scales, const int32_t* offsets, int32_t R, i
 }
 
 // Few rows per group on average: the operands swapped.  128 experts, H = 2048, I =
-// 768, cold L2, swapped against pair tiles.  Up: MXFP8 64 rows a group 90 / 107 us, 96
-// rows 109 / 111, 128 rows 135 / 116; MXFP4 64 rows 50.7 / 57.2, 96 rows 64.4 / 59.0.
-// Down: MXFP8 49 rows 43.0 / 53.7, 128 rows 61.8 / 63.7, 187 rows 80.4 / 73.6; MXFP4
-// 49 rows 29.8 / 38.7, 96 rows 39.8 / 42.1, 128 rows 46.9 / 45.5.
+// 768, cold L2, swapped against pair tiles.  Up with the swapped down product: MXFP8 96
+// rows a group 137 / 140 us, 128 rows 168 / 165; MXFP4 96 rows 90.4 / 95.3, 128 rows
+// 107 / 104.  Rows: MXFP8 K = 768 128 rows 51.6 / 59.0, 187 rows 67.0 / 68.4, K = 2048
+// 187 rows 114 / 118; MXFP4 K = 768 96 rows 37.0 / 40.9, 128 rows 43.7 / 44.0, 187
+// rows 57.4 / 50.9, K = 2048 63.0 / 64.5.
 // Rows of bf16 also where the swapped form's items (128 columns of up to 128 rows) are
 // no more than the SMs, and pair tiles would leave most SMs idle: one group of 1,024
 // rows, K = 2048, N = 1024, MXFP8 10.6 / 12.2, 2 x 512 rows, K = 256, N = 1536, MXFP4
 // 4.7 / 7.3.  (The up product gained nothing there: 2048 x 256 MXFP8 28.0 / 25.0.)
 bool mx_few(int fmt, int epi, int64_t rows, int64_t groups, int64_t n) {
-  if (epi == MX_SWIGLU) return rows <= (fmt == MOE_MXFP8 ? 96 : 80) * groups;
-  return rows <= (fmt == MOE_MXFP8 ? 128 : 112) * groups ||
+  if (epi == MX_SWIGLU) return rows <= 112 * groups;
+  return rows <= (fmt == MOE_MXFP8 ? 192 : 128) * groups ||
          (rows / 128 + groups) * ((n + 127) / 128) <= num_sms();
 }
 

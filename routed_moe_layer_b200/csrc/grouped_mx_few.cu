@@ -3,9 +3,9 @@
 //
 // With 15 rows an expert a 256-row tile spends its MMA time on padding and its
 // tile's fixed costs on little work, and the weights' stream, which bounds such
-// a call, waits for both.  Here 128 weight rows fill the MMA's M and at most C = 64
-// or 128 rows of a group its N (a multiple of 16), so that an MMA takes a quarter
-// or half of the time; one CTA per SM works alone, with 80 to 128 KB of weights in
+// a call, waits for both.  Here 128 weight rows fill the MMA's M and at most C = 64,
+// 96 or 128 rows of a group its N (a multiple of 16), so that an MMA takes a quarter
+// to half of the time; one CTA per SM works alone, with 80 to 128 KB of weights in
 // flight and two accumulators.
 //
 // Work item = (chunk of at most C rows of one group, 128 weight rows):
@@ -20,13 +20,18 @@
 // weights' scales (of the gate rows), warp 3 those of the up rows and of the
 // rows; warps 4..11 the epilogue.  Every wait is bounded (common.cuh).
 //
-// HBM bounds it: 1,920 rows of 128 groups, K = 1024, N = 1536, MXFP8: 38.4 us for 216
-// MB (5.6 TB/s, 0.87 of the measured copy; pair tiles 51 us); 1,536 items on 148 SMs
-// are 10.4 rounds, done in 11.  6,272 rows, K = 768, N = 2048: MXFP8 43.0 us for 238 MB
-// (5.5 TB/s; pair tiles 53.7), MXFP4 29.8 for 135 MB (4.5 TB/s; 38.7).  More stages than
-// these (8 rows, 5 SwiGLU) measured slower: 64 tokens of 128 experts MXFP8 103.5 us and
-// 108.3 or 109.7, MXFP4 60.0 and 63.0 or 64.5 (the first level cache gets what shared
-// memory leaves).
+// HBM bounds it: 1,920 rows of 128 groups, K = 1024, N = 1536, MXFP8: 36.0 us for 216
+// MB (6.0 TB/s, 0.93 of the measured copy; pair tiles 51 us); 6,272 rows, K = 768, N =
+// 2048: MXFP8 39.7 us for 238 MB (6.0 TB/s; pair tiles 53.7), MXFP4 28.0 for 135 MB
+// (4.8 TB/s; 38.7).  One row: the latency of a K step after the other, 8 rows of 8
+// groups, K = 8192, MXFP8: 14.7 us, 220 ns a stage.  That issue time was the bound
+// throughout before: with shared memory aligned at run time (addresses then live in
+// ordinary registers, and every barrier and descriptor costs more instructions) and one
+// K step a stage, 25 us, and the calls above 38.5, 43.0 and 29.8.
+//
+// Shared memory is kept small enough for a small kernel to start beside this one
+// (228 KB an SM): with 16 KB more the experts of 64 tokens took 108 us instead of 103,
+// because the next call's gathering copy, launched early, had to wait for this kernel.
 #include "mx_mma.cuh"
 
 namespace rmoe {
@@ -582,9 +587,11 @@ cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmA
 // MX_ROWS: rows per group, on average, from which items hold up to 128 rows and not
 // 64 (groups are uneven: fewer read their weights twice).  128 experts, K = 768, N =
 // 2048, 64 / 128 rows an item: MXFP8 15 rows a group 38.0 / 38.8 us, 32 rows 41.5 /
-// 40.2, 49 rows 48.9 / 43.0; MXFP4 25.4 / 25.4, 27.5 / 27.2, 32.1 / 29.8.  The up
-// product, with two accumulators a row, has room for 96 rows, which measured within
-// 5% of 64 either way.
+// 40.2, 49 rows 48.9 / 43.0; MXFP4 25.4 / 25.4, 27.5 / 27.2, 32.1 / 29.8.  MX_SWIGLU,
+// whose two accumulators leave room for 96: H = 2048, I = 768 with the down product
+// after it, 49 rows 120.8 / 120.3 MXFP8 and 74.5 / 74.7 MXFP4, 96 rows 145 / 137 and
+// 95.2 / 90.4.
+constexpr long long WIDE_UP_ROWS = 64;
 constexpr long long WIDE_ROWS = 24;
 
 // Bytes of a row above which items of 64 rows get a fourth stage: MXFP8 K = 2048, N =
@@ -598,7 +605,10 @@ cudaError_t launch_fmt(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxG
   if (args.tok_of)
     return epi == MX_SWIGLU ? launch<FMT, MX_SWIGLU, 64, 2, true>(tmW, tmX, args, stream)
                             : cudaErrorInvalidValue;
-  if (epi == MX_SWIGLU) return launch<FMT, MX_SWIGLU, 64, 2>(tmW, tmX, args, stream);
+  if (epi == MX_SWIGLU)
+    return args.rows > WIDE_UP_ROWS * args.groups
+               ? launch<FMT, MX_SWIGLU, 96, 4>(tmW, tmX, args, stream)
+               : launch<FMT, MX_SWIGLU, 64, 2>(tmW, tmX, args, stream);
   if (args.rows > WIDE_ROWS * args.groups)
     return launch<FMT, MX_ROWS, 128, 5>(tmW, tmX, args, stream);
   return args.k_bytes > DEEP_BYTES ? launch<FMT, MX_ROWS, 64, 4>(tmW, tmX, args, stream)

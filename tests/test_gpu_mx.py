@@ -404,15 +404,15 @@ def test_bad_offsets_are_reported_and_write_nothing_outside():
     assert (buf[:R] == K).all()
 
 
-# R, E, N, K of pair tiles: over 128 rows an expert, and more items of 128 x 128 than SMs
-PAIR_SHAPES = [(1000, 1, 2720, 352), (1500, 5, 1312, 1056), (3000, 3, 800, 96), (5600, 40, 416, 32),
+# R, E, N, K of pair tiles: over 192 rows an expert, and more items of 128 x 128 than SMs
+PAIR_SHAPES = [(1000, 1, 2720, 352), (1500, 5, 1312, 1056), (3000, 3, 800, 96), (7800, 40, 416, 32),
                (1100, 1, 2560, 2112), (700, 1, 3200, 160)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("R,E,N,K", PAIR_SHAPES)
 def test_grouped_mm_mx_pair_tiles(R, E, N, K, fmt):
-    assert R > 128 * E and (R // 128 + E) * -(-N // 128) > 148
+    assert R > 192 * E and (R // 128 + E) * -(-N // 128) > 148
     xc, xs, x = operands(R, K, fmt, R + K)
     wc, wsc, w = operands(N, K, fmt, N + K, lead=E, scale=0.1)
     lead, tail = 2, 3
@@ -587,7 +587,7 @@ def test_a_rows_bits_do_not_depend_on_the_other_rows(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("R,E", [(200, 2), (380, 4), (1400, 2)])
+@pytest.mark.parametrize("R,E", [(100, 2), (200, 2), (380, 4), (250, 2), (1400, 2)])
 def test_expert_rows_mx_between_the_forms(R, E, fmt):
     """Rows on either side of where the up and the down product change their form (1,400
     rows: both pair tiles): the bits of calls of at most 30 rows."""
