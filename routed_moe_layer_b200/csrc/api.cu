@@ -1181,13 +1181,12 @@ int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R, int32_t
   int* status = at<int>(workspace, 0);
   int* start = at<int>(workspace, align_up(sizeof(DevStatus)));
   int* tiles = at<int>(workspace, align_up(sizeof(DevStatus)) + align_up((size_t)(E + 1) * 4));
-  RMOE_TRY(launch_group_schedule(offsets, E, R, start, tiles, status, s));
   GemmArgs g;
   memset(&g, 0, sizeof(g));
   g.status = status;
   g.timeout_ns = DEFAULT_TIMEOUT_NS;
   g.alt_group = -1;
-  g.row_start = start;
+  g.row_start = offsets;
   g.num_groups = E;
   g.k_steps = (K + 63) / 64;  // past K both operands' tiles read zeros
   g.out = static_cast<__nv_bfloat16*>(y);
@@ -1199,6 +1198,9 @@ int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R, int32_t
   RMOE_TRY(make_tmap_3d(&tm_w, w, E, N, K));
   if ((int64_t)R <= 64LL * E) {  // few rows per expert: swapped operands, as moe_expert_rows
     const int chunk = (int64_t)R <= 20LL * E ? 32 : 128;
+    // the kernel checks the offsets itself: with the schedule's launch before it one token,
+    // K = 1024, N = 1536 took 13.7 us a call instead of 11.5
+    g.check_rows = R;
     RMOE_TRY(make_tmap_2d_box(&tm_x, x, R, K, 32));
     g.n_tiles = (N + 127) / 128;
     g.n_out_tile = 128;
@@ -1206,7 +1208,9 @@ int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R, int32_t
     return cuda_status(launch_grouped_gemm_swap(EPI_ROWSCALE, chunk, tm_w, tm_x, tm_w, tm_x, g,
                                                 (int)std::min<long long>(sms, items), s));
   }
+  RMOE_TRY(launch_group_schedule(offsets, E, R, start, tiles, status, s));
   RMOE_TRY(make_tmap_2d(&tm_x, x, R, K));
+  g.row_start = start;
   g.mtile_start = tiles;
   g.n_tiles = (N + 255) / 256;
   g.n_out_tile = 256;

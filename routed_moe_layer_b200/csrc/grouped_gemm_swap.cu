@@ -162,6 +162,44 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
   __syncthreads();
+  if (warp == 0 && args.check_rows > 0) {
+    // A caller's offsets.  The first bad one or none: whatever they are, the rows of every
+    // group then lie in [0, check_rows].
+    constexpr int PER = MAX_GROUPS / 32 + 1;
+    int at[PER], top = 0;
+    bool bad = false;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int g = lane * PER + q;
+      const int v = g <= groups ? st.row_start[g] : 0;
+      top = max(top, min(max(v, 0), args.check_rows));
+      at[q] = v;
+    }
+    int before = top;  // largest of this lane's offsets and those before them
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(FULL, before, off);
+      if (lane >= off) before = max(before, v);
+    }
+    before = __shfl_up_sync(FULL, before, 1);
+    int run = lane == 0 ? 0 : before;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int g = lane * PER + q;
+      if (g <= groups) {
+        run = max(run, min(max(at[q], 0), args.check_rows));
+        bad |= run != at[q];
+        st.row_start[g] = run;
+      }
+    }
+    if (lane == 0 && blockIdx.x == 0) {
+      args.status[0] = 0;
+      args.status[1] = 0;
+    }
+    if (__any_sync(FULL, bad) && lane == 0 && blockIdx.x == 0)
+      report_error(args.status, MOE_ERR_DEVICE_INDEX, 70);
+    __syncwarp();
+  }
   if (warp == 0) {  // exclusive prefix of chunks over groups (5 groups per lane)
     constexpr int PER = (MAX_GROUPS + 31) / 32;
     int loc[PER], sum = 0;

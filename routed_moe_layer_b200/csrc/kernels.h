@@ -114,6 +114,9 @@ struct GemmArgs {
   int dest_mul, dest_add;  //   row * dest_mul + dest_add
   int* status;
   unsigned long long timeout_ns;
+  int check_rows;          // swapped form: > 0: row_start are a caller's offsets, which are cut to
+                           //   [0, check_rows], made non-decreasing and reported when they had
+                           //   to be changed; the status word is cleared first
 };
 
 // A: 2D map over [rows, K] bf16, box 64 x 128, 128B swizzle.
