@@ -527,10 +527,14 @@ def rmsnorm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, eps: float = 
 # matrices has one more leading dimension in both.  These calls run on the device of their
 # tensors, on that device's current stream.
 
+_U8, _BF16, _I32 = torch.uint8, torch.bfloat16, torch.int32
+
+
 def _fmt(fmt: str) -> int:
-    if fmt not in MX_FORMATS:
+    f = MX_FORMATS.get(fmt) if isinstance(fmt, str) else None
+    if f is None:
         raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}, got {fmt!r}")
-    return MX_FORMATS[fmt]
+    return f
 
 
 def _at(t: Optional[torch.Tensor]):
@@ -578,13 +582,15 @@ def _ws_bytes(name: str, *sizes: int) -> int:
 
 
 def _need_mx(codes: torch.Tensor, scales: torch.Tensor, name: str, lead: tuple, rows: int,
-             K: int, fmt: int, dev: int):
-    u8 = torch.uint8
-    want_c = lead + (rows, K if fmt == 1 else K // 2)
-    want_s = lead + ((K + 127) // 128, rows, 4)
+             K: int, fmt: int, dev: int, shaped: bool = True):
+    """Codes and scales of a matrix or stack.  shaped False: the sizes are those of codes, whose
+    shape then is right (each test costs the host some 0.1 us)."""
+    u8 = _U8
+    want_c = (*lead, rows, K if fmt == 1 else K // 2)
+    want_s = (*lead, (K + 127) // 128, rows, 4)
     if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor)
-            and codes.dtype is u8 and scales.dtype is u8 and codes.shape == want_c
-            and scales.shape == want_s and codes.get_device() == dev and dev >= 0
+            and codes.dtype is u8 and scales.dtype is u8 and scales.shape == want_s
+            and (not shaped or codes.shape == want_c) and codes.get_device() == dev and dev >= 0
             and scales.get_device() == dev and codes.is_contiguous() and scales.is_contiguous()):
         _is(codes, f"{name}_codes", u8, want_c, dev)
         _is(scales, f"{name}_scales", u8, want_s, dev)
@@ -593,12 +599,15 @@ def _need_mx(codes: torch.Tensor, scales: torch.Tensor, name: str, lead: tuple, 
 def _matrices(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    shape = tuple(t.shape)
-    if len(shape) == 3:
-        return shape[0], shape[:1], shape[1], shape[2]
-    if len(shape) != 2:
+    shape = t.shape
+    n = len(shape)
+    if n == 2:
+        rows, K = shape
+        return 1, (), rows, K
+    if n != 3:
         raise ValueError(f"{name} must be a matrix or a stack of matrices")
-    return 1, (), shape[0], shape[1]
+    G, rows, K = shape
+    return G, (G,), rows, K
 
 
 def mx_quantize(x: torch.Tensor, fmt: str):
@@ -606,10 +615,11 @@ def mx_quantize(x: torch.Tensor, fmt: str):
     f = _fmt(fmt)
     G, lead, rows, K = _matrices(x, "x")
     dev = x.get_device()
-    _is(x, "x", torch.bfloat16, (*lead, rows, K), dev)
-    codes = (torch.empty_like(x, dtype=torch.uint8) if f == 1 else
-             x.new_empty(*lead, rows, K // 2, dtype=torch.uint8))
-    scales = x.new_empty(*lead, mx_words(K), rows, 4, dtype=torch.uint8)
+    if not (x.dtype is _BF16 and dev >= 0 and x.is_contiguous()):
+        _is(x, "x", _BF16, (*lead, rows, K), dev)
+    codes = (torch.empty_like(x, dtype=_U8) if f == 1 else
+             x.new_empty(*lead, rows, K // 2, dtype=_U8))
+    scales = codes.new_empty(*lead, (K + 127) // 128, rows, 4)
     _call("moe_mx_quantize", dev, x.data_ptr(), G, rows, K, f, codes.data_ptr(),
           scales.data_ptr())
     return codes, scales
@@ -621,8 +631,8 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: str) -> torch.
     G, lead, rows, K = _matrices(codes, "codes")
     K = K if f == 1 else 2 * K
     dev = codes.get_device()
-    _need_mx(codes, scales, "x", lead, rows, K, f, dev)
-    x = codes.new_empty(*lead, rows, K, dtype=torch.bfloat16)
+    _need_mx(codes, scales, "x", lead, rows, K, f, dev, False)
+    x = codes.new_empty(*lead, rows, K, dtype=_BF16)
     _call("moe_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), G, rows, K, f,
           x.data_ptr())
     return x
@@ -643,26 +653,28 @@ def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
     ``fmt`` (sum, xn, codes, scales), the MX form of xn.  ``sum_out`` receives
     the sum (x or residual: in place); without a residual the sum is x."""
     dev = _device(x, "x")
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be a matrix")
-    T, H = x.shape
-    _is(x, "x", torch.bfloat16, (T, H), dev)
+    T, H = shape
+    if not (x.dtype is _BF16 and dev >= 0 and x.is_contiguous()):
+        _is(x, "x", _BF16, shape, dev)
     f = 0 if fmt is None else _fmt(fmt)
     if residual is not None:
-        _is(residual, "residual", torch.bfloat16, (T, H), dev)
+        _is(residual, "residual", _BF16, shape, dev)
     if gamma is not None:
         _is(gamma, "gamma", torch.float32, (H,), dev)
     if sum_out is not None:
-        _is(sum_out, "sum_out", torch.bfloat16, (T, H), dev)
+        _is(sum_out, "sum_out", _BF16, shape, dev)
     total = sum_out
     if total is None:
         total = x if residual is None else torch.empty_like(x)
     xn = torch.empty_like(x)
     codes = scales = None
     if f:
-        codes = (torch.empty_like(x, dtype=torch.uint8) if f == 1 else
-                 x.new_empty(T, H // 2, dtype=torch.uint8))
-        scales = x.new_empty(mx_words(H), T, 4, dtype=torch.uint8)
+        codes = (torch.empty_like(x, dtype=_U8) if f == 1 else
+                 x.new_empty(T, H // 2, dtype=_U8))
+        scales = codes.new_empty((H + 127) // 128, T, 4)
     _call("moe_add_rmsnorm", dev, x.data_ptr(), _at(residual), _at(gamma), float(eps), T, H, f,
           None if total is x and residual is None else total.data_ptr(), xn.data_ptr(),
           _at(codes), _at(scales))
@@ -677,20 +689,22 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     groups keep what ``out`` holds (undefined without ``out``)."""
     dev = _device(x, "x")
     _device(w, "w")
-    if x.dim() != 2 or w.dim() != 3:
+    xs, ws = x.shape, w.shape
+    if len(xs) != 2 or len(ws) != 3:
         raise ValueError("x must be a matrix and w a stack of matrices")
-    R, K = x.shape
-    E, N, _ = w.shape
-    _is(x, "x", torch.bfloat16, (R, K), dev)
-    _is(w, "w", torch.bfloat16, (E, N, K), dev)
-    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
+    R, K = xs
+    E, N, _ = ws
+    if not (x.dtype is _BF16 and dev >= 0 and x.is_contiguous()):
+        _is(x, "x", _BF16, xs, dev)
+    _is(w, "w", _BF16, (E, N, K), dev)
+    _is(offsets, "offsets", _I32, (E + 1,), dev)
     if out is None:
         out = x.new_empty(R, N)
     else:
-        _is(out, "out", torch.bfloat16, (R, N), dev)
+        _is(out, "out", _BF16, (R, N), dev)
     if workspace is None:
         workspace = x.new_empty(_ws_bytes("moe_grouped_mm_workspace_bytes", R, E, N, K),
-                                dtype=torch.uint8)
+                                dtype=_U8)
     else:
         _workspace(workspace, dev)
     _call("moe_grouped_mm", dev, x.data_ptr(), offsets.data_ptr(), R, E, N, K, w.data_ptr(),
@@ -707,12 +721,12 @@ def _mx_out(R: int, N: int, x: torch.Tensor, dev: int, row_w, row_dest, out, out
     if row_w is not None:
         _is(row_w, "row_w", torch.float32, (R,), dev)
     if row_dest is not None:
-        _is(row_dest, "row_dest", torch.int32, (R,), dev)
+        _is(row_dest, "row_dest", _I32, (R,), dev)
     if out is None:
-        return x.new_empty(R if out_rows is None else out_rows, N, dtype=torch.bfloat16)
+        return x.new_empty(R if out_rows is None else out_rows, N, dtype=_BF16)
     if out_rows is None:
         out_rows = out.shape[0] if isinstance(out, torch.Tensor) and out.dim() == 2 else R
-    _is(out, "out", torch.bfloat16, (out_rows, N), dev)
+    _is(out, "out", _BF16, (out_rows, N), dev)
     return out
 
 
@@ -731,12 +745,12 @@ def grouped_mm_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.
         raise ValueError("x must be a matrix and w a stack of matrices")
     K = kb if f == 1 else 2 * kb
     dev = x_codes.get_device()
-    _need_mx(x_codes, x_scales, "x", (), R, K, f, dev)
-    _need_mx(w_codes, w_scales, "w", (E,), N, K, f, dev)
-    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
+    _need_mx(x_codes, x_scales, "x", (), R, K, f, dev, False)
+    _need_mx(w_codes, w_scales, "w", (E,), N, K, f, dev, False)
+    _is(offsets, "offsets", _I32, (E + 1,), dev)
     y = _mx_out(R, N, x_codes, dev, row_w, row_dest, out, out_rows)
     if workspace is None:
-        workspace = y.new_empty(256, dtype=torch.uint8)
+        workspace = x_codes.new_empty(256)
     else:
         _workspace(workspace, dev)
     _call("moe_grouped_mm_mx", dev, x_codes.data_ptr(), x_scales.data_ptr(), offsets.data_ptr(), R,
@@ -762,19 +776,19 @@ def expert_rows_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, offsets: torch
         raise ValueError("x must be a matrix and w13, w2 stacks of matrices")
     H, I = (hb if f == 1 else 2 * hb), I2 // 2
     dev = x_codes.get_device()
-    _need_mx(x_codes, x_scales, "x", (), T, H, f, dev)
+    _need_mx(x_codes, x_scales, "x", (), T, H, f, dev, False)
     _need_mx(w13_codes, w13_scales, "w13", (E,), 2 * I, H, f, dev)
     _need_mx(w2_codes, w2_scales, "w2", (E,), H, I, f, dev)
-    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
+    _is(offsets, "offsets", _I32, (E + 1,), dev)
     R = T
     if tok_of is not None:
         _device(tok_of, "tok_of")
         R = tok_of.numel()
-        _is(tok_of, "tok_of", torch.int32, (R,), dev)
+        _is(tok_of, "tok_of", _I32, (R,), dev)
     y = _mx_out(R, H, x_codes, dev, row_w, row_dest, y, y_rows)
     if workspace is None:
-        workspace = y.new_empty(_ws_bytes("moe_expert_rows_mx_workspace_bytes", R, H, E, I, f,
-                                          int(tok_of is not None)), dtype=torch.uint8)
+        workspace = x_codes.new_empty(_ws_bytes("moe_expert_rows_mx_workspace_bytes", R, H, E, I, f,
+                                                int(tok_of is not None)))
     else:
         _workspace(workspace, dev)
     _call("moe_expert_rows_mx", dev, x_codes.data_ptr(), x_scales.data_ptr(), T, _at(tok_of),
