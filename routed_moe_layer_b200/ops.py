@@ -746,7 +746,7 @@ def grouped_mm_mx(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.
     K = kb if f == 1 else 2 * kb
     dev = x_codes.get_device()
     _need_mx(x_codes, x_scales, "x", (), R, K, f, dev, False)
-    _need_mx(w_codes, w_scales, "w", (E,), N, K, f, dev, False)
+    _need_mx(w_codes, w_scales, "w", (E,), N, K, f, dev)  # K is the rows': the widths have to agree
     _is(offsets, "offsets", _I32, (E + 1,), dev)
     y = _mx_out(R, N, x_codes, dev, row_w, row_dest, out, out_rows)
     if workspace is None:

@@ -1,0 +1,102 @@
+"""Calls of the narrow-format operators that the Python functions refuse before
+the library is reached, tried on host tensors that say they are on a device
+(the library's calls are replaced by a list of those that got through)."""
+
+import pytest
+import torch
+
+from routed_moe_layer_b200 import ops
+
+BF16, U8, I32, F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
+
+
+class On(torch.Tensor):
+    """A host tensor that says it is on a device."""
+
+    on = 0
+
+    def get_device(self):
+        return self.on
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+def on(*shape, dtype=U8, dev=0):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(On)
+    t.on = dev
+    return t
+
+
+@pytest.fixture
+def called(monkeypatch):
+    """Names of the entry points that a call reached."""
+    names = []
+    monkeypatch.setattr(ops, "_call", lambda name, *a: names.append(name))
+    monkeypatch.setattr(ops, "_ws_bytes", lambda *a: 256)
+    return names
+
+
+def mx(rows, K, fmt, lead=()):
+    """Codes and scales of zeros, laid out for rows of K elements."""
+    return (on(*lead, rows, K if fmt == "mxfp8" else K // 2), on(*lead, -(-K // 128), rows, 4))
+
+
+# the rows' format and K, the weights' format and K: the scales' shapes are those of
+# the rows' K in all of them, so the codes alone tell
+WRONG_WIDTHS = [
+    ("mxfp8", 1024, "mxfp4", 1024),  # half the bytes that K elements take
+    ("mxfp4", 1024, "mxfp8", 1024),  # twice the bytes
+    ("mxfp8", 1024, "mxfp8", 928),   # another K in the same word of scales
+    ("mxfp4", 1024, "mxfp4", 992),
+    ("mxfp8", 96, "mxfp8", 1),
+    ("mxfp8", 96, "mxfp8", 128),
+]
+
+
+@pytest.mark.parametrize("fmt,K,w_fmt,w_K", WRONG_WIDTHS)
+def test_grouped_mm_mx_refuses_weights_of_another_width(called, fmt, K, w_fmt, w_K):
+    E, N = 2, 64
+    x, xs = mx(8, K, fmt)
+    off = on(E + 1, dtype=I32)
+    w, ws = mx(N, K, fmt, (E,))
+    out = on(8, N, dtype=BF16)
+    ops.grouped_mm_mx(x, xs, w, ws, off, fmt, out=out)  # of the same width: goes through
+    assert called == ["moe_grouped_mm_mx"]
+    bad = mx(N, w_K, w_fmt, (E,))[0]
+    assert bad.shape != w.shape
+    with pytest.raises(ValueError, match="w_codes must have shape"):
+        ops.grouped_mm_mx(x, xs, bad, ws, off, fmt, out=out)
+    assert called == ["moe_grouped_mm_mx"]
+
+
+@pytest.mark.parametrize("fmt,K,w_fmt,w_K", WRONG_WIDTHS)
+def test_expert_rows_mx_refuses_weights_of_another_width(called, fmt, K, w_fmt, w_K):
+    E, other = 2, 64  # K as H for w13, as I for w2
+    off = on(E + 1, dtype=I32)
+    bad = mx(2 * other, w_K, w_fmt, (E,))[0]
+    for H, I in ((K, other), (other, K)):
+        x, xs = mx(8, H, fmt)
+        w13, w13s = mx(2 * I, H, fmt, (E,))
+        w2, w2s = mx(H, I, fmt, (E,))
+        y = on(8, H, dtype=BF16)
+        called.clear()
+        ops.expert_rows_mx(x, xs, off, w13, w13s, w2, w2s, None, fmt, y=y)
+        assert called == ["moe_expert_rows_mx"]
+        with pytest.raises(ValueError, match="must have shape"):
+            if H == K:
+                ops.expert_rows_mx(x, xs, off, bad, w13s, w2, w2s, None, fmt, y=y)
+            else:
+                ops.expert_rows_mx(x, xs, off, w13, w13s, bad[:, :H], w2s, None, fmt, y=y)
+        assert called == ["moe_expert_rows_mx"]
+
+
+@pytest.mark.parametrize("w_K", [1, 32, 96, 160, 256])
+def test_grouped_mm_refuses_weights_of_another_width(called, w_K):
+    x, off = on(8, 128, dtype=BF16), on(3, dtype=I32)
+    ops.grouped_mm(x, on(2, 64, 128, dtype=BF16), off, out=on(8, 64, dtype=BF16))
+    assert called == ["moe_grouped_mm"]
+    with pytest.raises(ValueError, match="w must have shape"):
+        ops.grouped_mm(x, on(2, 64, w_K, dtype=BF16), off, out=on(8, 64, dtype=BF16))
+    assert called == ["moe_grouped_mm"]
