@@ -808,13 +808,22 @@ def forward_mx(x: torch.Tensor, Wr: torch.Tensor, bias: torch.Tensor, w13: tuple
     the bf16 shared expert, combine_rows); returns out bf16 [T,H].
     w13, w2: (codes, scales) of [E,2I,H] and [E,H,I]; x_mx: (codes, scales) of x
     where add_rmsnorm has made them, else x is quantised here."""
-    ids, w = route(x, Wr, bias, cfg, token_mask=token_mask)
-    p = permute(ids, cfg, topk_w=w)
-    codes, scales = mx_quantize(x, fmt) if x_mx is None else x_mx
-    y = expert_rows_mx(codes, scales, p["expert_offsets"], *w13, *w2, None, fmt, row_w=p["w_of"],
-                       tok_of=p["tok_of"])
-    shared = dense_ffn(x, ws13, ws2) if cfg.I_shared > 0 else None
-    return combine_rows(y, p["row_of"], cfg.top_k, shared=shared, residual=residual, out=out)
+    _need(x, "x", _BF16, (cfg.T, cfg.H))
+    dev = x.get_device()
+    shared_w = (("ws13", ws13), ("ws2", ws2)) if cfg.I_shared > 0 else ()  # else not used
+    for name, t in (("Wr", Wr), ("bias", bias), *shared_w, ("residual", residual), ("out", out),
+                    ("token_mask", token_mask)):
+        if t is not None and _device(t, name) != dev:
+            raise ValueError(f"all tensors must be on cuda:{dev}, {name} is on {t.device}")
+    # route, permute, dense_ffn and combine_rows run on the current device
+    with torch.cuda.device(dev):
+        ids, w = route(x, Wr, bias, cfg, token_mask=token_mask)
+        p = permute(ids, cfg, topk_w=w)
+        codes, scales = mx_quantize(x, fmt) if x_mx is None else x_mx
+        y = expert_rows_mx(codes, scales, p["expert_offsets"], *w13, *w2, None, fmt,
+                           row_w=p["w_of"], tok_of=p["tok_of"])
+        shared = dense_ffn(x, ws13, ws2) if cfg.I_shared > 0 else None
+        return combine_rows(y, p["row_of"], cfg.top_k, shared=shared, residual=residual, out=out)
 
 
 def read_device_status(workspace: torch.Tensor):

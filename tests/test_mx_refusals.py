@@ -100,3 +100,71 @@ def test_grouped_mm_refuses_weights_of_another_width(called, w_K):
     with pytest.raises(ValueError, match="w must have shape"):
         ops.grouped_mm(x, on(2, 64, w_K, dtype=BF16), off, out=on(8, 64, dtype=BF16))
     assert called == ["moe_grouped_mm"]
+
+
+STEPS = ("route", "permute", "mx_quantize", "expert_rows_mx", "dense_ffn", "combine_rows")
+
+
+@pytest.fixture
+def steps(monkeypatch):
+    """(step, current device) of every step that forward_mx takes; device 0 is current
+    outside of it."""
+    taken, current = [], [0]
+
+    class Device:  # torch.cuda.device
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    def step(name, result):
+        def f(*a, **k):
+            taken.append((name, current[-1]))
+            return result
+        monkeypatch.setattr(ops, name, f)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    step("route", (None, None))
+    step("permute", dict(expert_offsets=None, row_of=None, tok_of=None, w_of=None))
+    step("mx_quantize", (None, None))
+    for name in STEPS[3:]:
+        step(name, name)
+    return taken
+
+
+def block(dev, T=6, H=128, Is=64, E=8, I=32):
+    cfg = ops.BlockConfig(T=T, H=H, E=E, I=I, I_shared=Is, top_k=2)
+    return dict(x=on(T, H, dtype=BF16, dev=dev), Wr=on(E, H, dtype=F32, dev=dev),
+                bias=on(E, dtype=F32, dev=dev), w13=(None, None), w2=(None, None),
+                ws13=on(2 * Is, H, dtype=BF16, dev=dev), ws2=on(H, Is, dtype=BF16, dev=dev), cfg=cfg,
+                fmt="mxfp8")
+
+
+@pytest.mark.parametrize("dev", [0, 1])
+def test_forward_mx_takes_every_step_on_its_tensors_device(steps, dev):
+    assert ops.forward_mx(**block(dev)) == "combine_rows"
+    assert steps == [(name, dev) for name in STEPS]
+
+
+@pytest.mark.parametrize("name", ["Wr", "bias", "ws13", "ws2", "residual", "out", "token_mask"])
+def test_forward_mx_refuses_tensors_of_two_devices(steps, name):
+    a = block(1) | {"residual": on(6, 128, dtype=BF16, dev=1), "out": on(6, 128, dtype=BF16, dev=1),
+                    "token_mask": on(6, dev=1)}
+    assert ops.forward_mx(**a) == "combine_rows"
+    steps.clear()
+    a[name].on = 0
+    with pytest.raises(ValueError, match=f"cuda:1, {name} is on"):
+        ops.forward_mx(**a)
+    with pytest.raises(TypeError, match=f"{name} must be a tensor"):
+        ops.forward_mx(**a | {name: "x"})
+    assert not steps
+
+
+def test_forward_mx_without_a_shared_expert_does_not_look_at_its_weights(steps):
+    a = block(0) | {"ws13": None, "ws2": on(1, dev=1)}
+    a["cfg"].I_shared = 0
+    assert ops.forward_mx(**a) == "combine_rows"
+    assert "dense_ffn" not in [name for name, _ in steps]
