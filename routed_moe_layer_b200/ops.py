@@ -815,11 +815,15 @@ def forward_mx(x: torch.Tensor, Wr: torch.Tensor, bias: torch.Tensor, w13: tuple
                     ("token_mask", token_mask)):
         if t is not None and _device(t, name) != dev:
             raise ValueError(f"all tensors must be on cuda:{dev}, {name} is on {t.device}")
+    if x_mx is not None:  # one row of codes for every token: a missing one would count as zeros
+        codes, scales = x_mx
+        _need_mx(codes, scales, "x", (), cfg.T, cfg.H, _fmt(fmt), dev)
     # route, permute, dense_ffn and combine_rows run on the current device
     with torch.cuda.device(dev):
         ids, w = route(x, Wr, bias, cfg, token_mask=token_mask)
         p = permute(ids, cfg, topk_w=w)
-        codes, scales = mx_quantize(x, fmt) if x_mx is None else x_mx
+        if x_mx is None:
+            codes, scales = mx_quantize(x, fmt)
         y = expert_rows_mx(codes, scales, p["expert_offsets"], *w13, *w2, None, fmt,
                            row_w=p["w_of"], tok_of=p["tok_of"])
         shared = dense_ffn(x, ws13, ws2) if cfg.I_shared > 0 else None

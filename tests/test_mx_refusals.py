@@ -168,3 +168,23 @@ def test_forward_mx_without_a_shared_expert_does_not_look_at_its_weights(steps):
     a["cfg"].I_shared = 0
     assert ops.forward_mx(**a) == "combine_rows"
     assert "dense_ffn" not in [name for name, _ in steps]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("T,H", [(5, 128), (7, 128), (0, 128), (6, 64), (6, 160), (6, 256)])
+def test_forward_mx_refuses_codes_of_other_tokens(steps, T, H, fmt):
+    a = block(0) | {"fmt": fmt}
+    good, bad = mx(6, 128, fmt), mx(T, H, fmt)
+    assert ops.forward_mx(**a, x_mx=good) == "combine_rows"
+    assert "mx_quantize" not in [name for name, _ in steps]
+    steps.clear()
+    for x_mx in (bad, (bad[0], good[1]), (good[0], bad[1])):
+        if [t.shape for t in x_mx] != [t.shape for t in good]:
+            with pytest.raises(ValueError, match="must have shape"):
+                ops.forward_mx(**a, x_mx=x_mx)
+    other = "mxfp4" if fmt == "mxfp8" else "mxfp8"
+    with pytest.raises(ValueError, match="x_codes must have shape"):
+        ops.forward_mx(**a, x_mx=mx(6, 128, other))
+    with pytest.raises(ValueError, match="cuda:0"):
+        ops.forward_mx(**a, x_mx=(on(*good[0].shape, dev=1), good[1]))
+    assert not steps
