@@ -715,6 +715,8 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
 def _workspace(t, dev: int):
     if _device(t, "workspace") != dev:
         raise ValueError(f"workspace must be on cuda:{dev}, got {t.device}")
+    if not t.is_contiguous():  # an expanded tensor has more elements than bytes behind it
+        raise ValueError("workspace must be contiguous")
 
 
 def _mx_out(R: int, N: int, x: torch.Tensor, dev: int, row_w, row_dest, out, out_rows):

@@ -188,3 +188,27 @@ def test_forward_mx_refuses_codes_of_other_tokens(steps, T, H, fmt):
     with pytest.raises(ValueError, match="cuda:0"):
         ops.forward_mx(**a, x_mx=(on(*good[0].shape, dev=1), good[1]))
     assert not steps
+
+
+def test_workspaces_that_are_not_whole_are_refused(called):
+    E, N, K = 2, 64, 64
+    x, off = on(8, K, dtype=BF16), on(E + 1, dtype=I32)
+    c, s = mx(8, K, "mxfp8")
+    w, ws = mx(N, K, "mxfp8", (E,))
+    w13, w13s = mx(2 * N, K, "mxfp8", (E,))
+    calls = (
+        lambda k: ops.grouped_mm(x, on(E, N, K, dtype=BF16), off, out=on(8, N, dtype=BF16), workspace=k),
+        lambda k: ops.grouped_mm_mx(c, s, w, ws, off, "mxfp8", out=on(8, N, dtype=BF16), workspace=k),
+        lambda k: ops.expert_rows_mx(c, s, off, w13, w13s, w, ws, None, "mxfp8",
+                                     y=on(8, K, dtype=BF16), workspace=k),
+    )
+    one = torch.zeros(1, dtype=U8).expand(1 << 16).as_subclass(On)  # 65,536 elements of one byte
+    for i, call in enumerate(calls):
+        call(on(1 << 16))
+        assert len(called) == i + 1
+        for bad in (one, on(1 << 16)[::2]):
+            with pytest.raises(ValueError, match="workspace must be contiguous"):
+                call(bad)
+        with pytest.raises(ValueError, match="workspace must be on cuda:0"):
+            call(on(1 << 16, dev=1))
+        assert len(called) == i + 1
