@@ -414,7 +414,8 @@ MOE_API size_t moe_grouped_mm_mx_workspace_bytes(int32_t R, int32_t E, int32_t N
  *           (empty groups allowed; rows outside the groups are left as they were)
  * E in 1..128; N and K multiples of 32 (<= 16384).  Offsets that break their
  * rule leave MOE_ERR_DEVICE_INDEX in the status word (moe_read_device_status)
- * and y undefined; no access leaves the operands.  y must not overlap x or w. */
+ * and y undefined; no access leaves the operands.  y must not overlap x or w
+ * (MOE_ERR_INVALID_ARG). */
 MOE_API int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R, int32_t E,
                                int32_t N, int32_t K, const void* w, void* y, void* workspace,
                                size_t workspace_bytes, void* stream);
@@ -427,7 +428,8 @@ MOE_API int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R,
  *   row_w    device fp32 [R] or NULL (1)
  *   row_dest device int32 [R], distinct rows of y, or NULL (dest(r) = r); a row
  *            whose destination lies outside [0, y_rows) is not stored
- *   y        device bf16 [y_rows, N] (y_rows >= R without row_dest)
+ *   y        device bf16 [y_rows, N] (y_rows >= R without row_dest); must not
+ *            overlap the operands' codes or scales (MOE_ERR_INVALID_ARG)
  * Offsets, sizes, errors and workspace as moe_grouped_mm.  A row's bits do not
  * depend on the other rows of the call (the kernels for few and for many rows
  * per expert give the same). */
@@ -451,7 +453,8 @@ MOE_API size_t moe_expert_rows_mx_workspace_bytes(int32_t R, int32_t H, int32_t 
  *   tok_of   device int32 [R]: x_r is row tok_of[r] of x (a token outside [0, T)
  *            counts as zeros); NULL: x holds the rows already grouped, T == R
  *   w13_*    E matrices [2I, H], gate rows then up rows; w2_* E matrices [H, I]
- *   row_w, row_dest, y, y_rows, offsets and errors as moe_grouped_mm_mx
+ *   row_w, row_dest, y, y_rows, offsets and errors as moe_grouped_mm_mx (y must
+ *            not overlap the weights, nor be x_codes)
  * H and I multiples of 32 (<= 16384).  With row_dest = t*top_k + j and
  * moe_combine_rows this is the routed half of the block on narrow operands. */
 MOE_API int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int32_t T,

@@ -655,6 +655,12 @@ int32_t forward_fp8_impl(const void* x, const float* Wr, const float* bias, cons
 // ------------------------------------------------------------------ MX operands
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// Whether [a, a + na) and [b, b + nb) have a byte in common.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + nb && q < p + na;
+}
+
 bool mx_fmt_ok(int32_t fmt) { return fmt == MOE_MXFP8 || fmt == MOE_MXFP4; }
 
 // A matrix of rows x K elements, or a stack of them.
@@ -663,6 +669,14 @@ int32_t check_mx(int32_t groups, int32_t rows, int32_t K, int32_t fmt) {
   if (K % 32 != 0 || K > MAX_DIM || (int64_t)groups * rows > INT32_MAX / 2)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
+}
+
+// Whether [p, p + n) overlaps the codes or scales of `rows` rows of K elements (all
+// matrices of a stack together).
+bool overlaps_mx(const void* p, size_t n, const uint8_t* codes, const uint8_t* scales, size_t rows,
+                 int32_t K, int32_t fmt) {
+  return overlap(p, n, codes, rows * mx_row_bytes(K, fmt)) ||
+         overlap(p, n, scales, rows * mx_words(K) * 4);
 }
 
 // y [R,N] = rows [R,K] times the matrix [N,K] of their group.
@@ -1175,8 +1189,11 @@ int32_t moe_grouped_mm(const void* x, const int32_t* offsets, int32_t R, int32_t
   const int32_t st = check_grouped(R, E, N, K);
   if (st != MOE_OK) return st;
   if (R == 0) return MOE_OK;
-  if (!x || !offsets || !w || !y || y == x || y == w) return MOE_ERR_INVALID_ARG;
+  if (!x || !offsets || !w || !y) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 32) || !aligned(offsets, 4))
+    return MOE_ERR_INVALID_ARG;
+  const size_t y_bytes = (size_t)R * N * 2;
+  if (overlap(y, y_bytes, x, (size_t)R * K * 2) || overlap(y, y_bytes, w, (size_t)E * N * K * 2))
     return MOE_ERR_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, moe_grouped_mm_workspace_bytes(R, E, N, K)))
     return MOE_ERR_WORKSPACE;
@@ -1237,13 +1254,15 @@ int32_t moe_grouped_mm_mx(const uint8_t* x_codes, const uint8_t* x_scales, const
   if (st != MOE_OK) return st;
   if (!mx_fmt_ok(fmt) || y_rows < 0) return MOE_ERR_INVALID_ARG;
   if (R == 0) return MOE_OK;
-  if (!x_codes || !x_scales || !offsets || !w_codes || !w_scales || !y || y == x_codes ||
-      y == w_codes)
-    return MOE_ERR_INVALID_ARG;
+  if (!x_codes || !x_scales || !offsets || !w_codes || !w_scales || !y) return MOE_ERR_INVALID_ARG;
   if (!row_dest && y_rows < R) return MOE_ERR_INVALID_ARG;
   if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(y, 32) || !aligned(x_scales, 4) ||
       !aligned(w_scales, 16) || !aligned(offsets, 4) || !aligned(row_w, 4) ||
       !aligned(row_dest, 4))
+    return MOE_ERR_INVALID_ARG;
+  const size_t y_bytes = (size_t)y_rows * N * 2;
+  if (overlaps_mx(y, y_bytes, x_codes, x_scales, R, K, fmt) ||
+      overlaps_mx(y, y_bytes, w_codes, w_scales, (size_t)E * N, K, fmt))
     return MOE_ERR_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, moe_grouped_mm_mx_workspace_bytes(R, E, N, K)))
     return MOE_ERR_WORKSPACE;
@@ -1284,6 +1303,10 @@ int32_t moe_expert_rows_mx(const uint8_t* x_codes, const uint8_t* x_scales, int3
       !aligned(y, 32) || !aligned(x_scales, 4) || !aligned(w13_scales, 16) ||
       !aligned(w2_scales, 16) || !aligned(offsets, 4) || !aligned(tok_of, 4) ||
       !aligned(row_w, 4) || !aligned(row_dest, 4))
+    return MOE_ERR_INVALID_ARG;
+  const size_t y_bytes = (size_t)y_rows * H * 2;
+  if (overlaps_mx(y, y_bytes, w13_codes, w13_scales, (size_t)E * 2 * I, H, fmt) ||
+      overlaps_mx(y, y_bytes, w2_codes, w2_scales, (size_t)E * H, I, fmt))
     return MOE_ERR_INVALID_ARG;
   const MxExpertsLayout L = mx_experts_layout(R, H, I, fmt, tok_of != nullptr);
   if (!ws_ok(workspace, workspace_bytes, L.total)) return MOE_ERR_WORKSPACE;
