@@ -191,24 +191,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
   }
-  if (warp == 1) {
-    tmem_alloc(&st.tmem_base, TMEM_COLS);
-    tmem_relinquish();
-  }
   // What comes before reads nothing that an earlier kernel writes.  After the up
   // product (args.after_up) only its rows have to be waited for: it lets this
   // kernel start when all that came before it was complete, so the group table
   // and the weights can be read while it runs.
   const bool early = EPI == MX_ROWS && args.after_up != 0;
   if (!early) pdl_wait();
-  pdl_launch_dependents();  // not before pdl_wait: the kernel after may be such a one
   const int total = mx_group_table<C>(args, st.groups) * args.n_tiles;
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem_base = uniform(st.tmem_base);
   const WaitCtx wc{&st.abort_flag, args.status, args.timeout_ns};
   const int first = blockIdx.x, step = gridDim.x;
+  uint32_t tmem_base = 0;  // warp 1 and the epilogue
   if (first < total) {
     const int k_steps = (args.k_bytes + KB - 1) / KB;
     const int* mts = st.groups.mt_start;
@@ -293,6 +285,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     } else if (warp == 1) {
       // ------------------------------------------------ scales to TMEM and MMAs
+      // All of TMEM, which has no wait with a limit: behind the wait for the kernels
+      // before, one of which could otherwise be waiting for it, and before the kernel
+      // after may start, which could otherwise take it first and wait for this one.
+      // The first operands are on their way meanwhile.
+      if (early) pdl_wait();
+      tmem_alloc(&st.tmem_base, TMEM_COLS);
+      tmem_relinquish();
+      tc_fence_before_sync();
+      warps_sync<1 + EPI_WARPS>(2);
+      tc_fence_after_sync();
+      tmem_base = uniform(st.tmem_base);
+      // (also not before the wait because the kernel after may be an early one)
+      pdl_launch_dependents();
       constexpr int SF_STEPS = SF_WORDS / S::kWords;  // K steps per buffer of scales
       int stage = 0, buf = 0, acc = 0;
       uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
@@ -428,6 +433,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
       // ------------------------------------------------ epilogue warps 4..11
       if (early) pdl_wait();
+      warps_sync<1 + EPI_WARPS>(2);
+      tc_fence_after_sync();
+      tmem_base = uniform(st.tmem_base);
       const int q = warp & 3, part = (warp - EPI_WARP0) >> 2;
       constexpr int COPIES = C / EPI_WARPS;  // MX_ROWS: rows that a warp copies, one a lane
       const uint32_t out = smem0 + S::kOffOut;
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 1 && first < total) {
     tc_fence_after_sync();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
