@@ -28,6 +28,20 @@ cudaError_t set_smem_limit_per_device(void (*k)(KArgs...), int bytes,
   return e;
 }
 
+// Runs encode, a call of cuTensorMapEncodeTiled.  That driver call fails on a host
+// thread without a current context, and a thread gets one by its first runtime call
+// that needs it, which in a new thread may be none before this: then the device is
+// set, to the one that is current anyway, and the call repeated.
+template <typename F>
+cudaError_t encode_in_context(F&& encode) {
+  if (encode() == CUDA_SUCCESS) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return e;
+  return encode() == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // Launches kernel k chained to the previous work of the stream (programmatic
 // stream serialisation; the kernel itself waits with pdl_wait before reading
 // what its predecessors wrote).

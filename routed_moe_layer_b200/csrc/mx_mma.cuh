@@ -242,11 +242,11 @@ inline cudaError_t encode_tmap(CUtensorMap* map, CUtensorMapDataType type, int r
   auto fn = mx_encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r =
-      fn(map, type, rank, const_cast<void*>(base), dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode_in_context([&] {
+    return fn(map, type, rank, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 }  // namespace rmoe
