@@ -716,6 +716,9 @@ MxGemmArgs mx_args(const uint8_t* a_scales, const int32_t* offsets, int32_t R, i
 // no more than the SMs, and pair tiles would leave most SMs idle: one group of 1,024
 // rows, K = 2048, N = 1024, MXFP8 10.6 / 12.2, 2 x 512 rows, K = 256, N = 1536, MXFP4
 // 4.7 / 7.3.  (The up product gained nothing there: 2048 x 256 MXFP8 28.0 / 25.0.)
+// The host knows the average alone.  Experts with every token on the same 8 of 128,
+// as here / on pair tiles: 784 tokens MXFP8 61.4 / 67.3 us, MXFP4 42.9 / 39.3; 1,536
+// tokens 93.7 / 73.0, 66.0 / 48.6.
 bool mx_few(int fmt, int epi, int64_t rows, int64_t groups, int64_t n) {
   if (epi == MX_SWIGLU) return rows <= 112 * groups;
   return rows <= (fmt == MOE_MXFP8 ? 192 : 128) * groups ||
@@ -733,6 +736,10 @@ cudaError_t mx_product(int fmt, int epi, const void* a, const void* b, const MxG
 // itself / from a copy: MXFP8 2 rows an expert 80.5 / 86.5 us, 4 rows 92.6 / 96.9, 8
 // rows 109.3 / 107.5, 15 rows 168 / 111; MXFP4 45.9 / 50.0, 52.6 / 55.8, 61.8 / 61.2,
 // 92 / 63.
+// By the average too, although the copy is far better where few experts hold all the
+// rows (then a few CTAs issue every box): every token on the same 8 experts, 16 tokens
+// (1 row an expert on average) MXFP8 23.8 / 16.7 us, MXFP4 15.6 / 12.7; 64 tokens (4
+// rows) 67.6 / 19.4, 38.2 / 15.2.
 constexpr int64_t GATHER_ROWS_PER_EXPERT = 4;
 bool gather_in_product(int32_t R, int32_t E) { return R <= GATHER_ROWS_PER_EXPERT * (int64_t)E; }
 

@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   __syncthreads();
   if (warp == 0 && args.check_rows > 0) {
-    // A caller's offsets.  The first bad one or none: whatever they are, the rows of every
-    // group then lie in [0, check_rows].
+    // A caller's offsets: cut to [0, check_rows] and raised to the largest before them, so
+    // that the rows of every group lie in that range whatever they are.  Ones that this
+    // changes are reported.
     constexpr int PER = MAX_GROUPS / 32 + 1;
     int at[PER], top = 0;
     bool bad = false;

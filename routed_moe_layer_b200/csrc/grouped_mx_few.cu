@@ -18,7 +18,8 @@
 // tcgen05.cp wants (mx_mma.cuh), 8 words a row at a time, two buffers.
 // Warp roles: warp 0 TMA loads; warp 1 TMEM, scales to TMEM, MMAs; warp 2 the
 // weights' scales (of the gate rows), warp 3 those of the up rows and of the
-// rows; warps 4..11 the epilogue.  Every wait is bounded (common.cuh).
+// rows; warps 4..11 the epilogue.  Every wait but that for tensor memory is bounded
+// (common.cuh).
 //
 // HBM bounds it: 1,920 rows of 128 groups, K = 1024, N = 1536, MXFP8: 36.0 us for 216
 // MB (6.0 TB/s, 0.93 of the measured copy; pair tiles 51 us); 6,272 rows, K = 768, N =
@@ -29,9 +30,12 @@
 // ordinary registers, and every barrier and descriptor costs more instructions) and one
 // K step a stage, 25 us, and the calls above 38.5, 43.0 and 29.8.
 //
-// Shared memory is kept small enough for a small kernel to start beside this one
-// (228 KB an SM): with 16 KB more the experts of 64 tokens took 108 us instead of 103,
-// because the next call's gathering copy, launched early, had to wait for this kernel.
+// Shared memory: rows of bf16 177 KB (items of 64 rows, three stages), 225 KB (four) and
+// 209 KB (items of 128 rows), SwiGLU 185 KB (64 rows) and 201 KB (96 rows).  Every form
+// leaves room on its SM (228 KB, of which each block takes 1 KB more than its own) for
+// a block without shared memory, as those of the next call's gathering copy are, which
+// starts early: with less the experts of 64 tokens took 108 us instead of 103, because
+// the copy had to wait for this kernel.
 #include "mx_mma.cuh"
 
 namespace rmoe {
@@ -581,7 +585,7 @@ template <int FMT, int EPI, int C, int STAGES, bool GATHER = false>
 cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& args,
                    cudaStream_t stream) {
   constexpr size_t smem = Shape<FMT, EPI, C, STAGES>::kOffTail + sizeof(SmemTail);
-  static_assert(smem <= 227 * 1024, "shared memory");
+  static_assert(smem + 2 * 1024 <= 228 * 1024, "shared memory: a small kernel's block beside it");
   static std::atomic<int> smem_set[MAX_DEVICES];
   auto kernel = grouped_mx_few_kernel<FMT, EPI, C, STAGES, GATHER>;
   const cudaError_t e = set_smem_limit_per_device(kernel, (int)smem, smem_set);
