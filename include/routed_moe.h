@@ -380,12 +380,14 @@ typedef enum {
  * ties to the even code.  A block that holds a NaN or an infinity gets the
  * scale byte 255 (NaN) and codes 0: every product with it is NaN.
  *   x      device bf16 [groups, rows, K], groups * rows < 2^30
- *   codes, scales  out, as above (bytes of blocks past K are written as 0) */
+ *   codes, scales  out, as above (bytes of blocks past K are written as 0); they
+ *            must not overlap x or each other (MOE_ERR_INVALID_ARG) */
 MOE_API int32_t moe_mx_quantize(const void* x, int32_t groups, int32_t rows, int32_t K,
                                 int32_t fmt, uint8_t* codes, uint8_t* scales, void* stream);
 
 /* MX -> bf16: x = bf16(element * 2^p), NaN for a block of scale byte 255.
- * Exact for what moe_mx_quantize gives wherever bf16 holds the value. */
+ * Exact for what moe_mx_quantize gives wherever bf16 holds the value.  x must not
+ * overlap codes or scales (MOE_ERR_INVALID_ARG). */
 MOE_API int32_t moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t groups,
                                   int32_t rows, int32_t K, int32_t fmt, void* x, void* stream);
 
@@ -398,7 +400,8 @@ MOE_API int32_t moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, i
  *   sum      device bf16 [T,H] out or NULL; may be x or residual (in place)
  *   xn       device bf16 [T,H] out, or NULL when codes are wanted alone
  *   fmt      0: no codes (codes, scales NULL); MOE_MXFP8 or MOE_MXFP4
- * H a multiple of 64 (<= 16384).  A row's outputs depend on that row alone. */
+ * H a multiple of 64 (<= 16384).  A row's outputs depend on that row alone.  But for
+ * sum in place, no output may overlap another or an input (MOE_ERR_INVALID_ARG). */
 MOE_API int32_t moe_add_rmsnorm(const void* x, const void* residual, const float* gamma,
                                 float eps, int32_t T, int32_t H, int32_t fmt, void* sum, void* xn,
                                 uint8_t* codes, uint8_t* scales, void* stream);

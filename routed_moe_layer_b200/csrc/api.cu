@@ -1155,9 +1155,22 @@ int32_t moe_add_rmsnorm(const void* x, const void* residual, const float* gamma,
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(sum, 16) ||
       !aligned(xn, 16) || !aligned(codes, 16) || !aligned(scales, 4))
     return MOE_ERR_INVALID_ARG;
-  // every row is read before it is written, so sum may be x or the residual;
-  // no other output may be anything else that the call reads or writes
-  if (xn && (xn == x || xn == residual || xn == sum)) return MOE_ERR_INVALID_ARG;
+  // A thread reads what it writes of sum before it writes, so sum may be x or the
+  // residual, but not lie over other rows of them; no other output may lie over
+  // anything else that the call reads or writes.
+  const size_t n = (size_t)T * H * 2;
+  if (sum && ((sum != x && overlap(sum, n, x, n)) ||
+              (residual && sum != residual && overlap(sum, n, residual, n))))
+    return MOE_ERR_INVALID_ARG;
+  struct {
+    const void* p;
+    size_t n;
+  } const r[] = {{xn, n}, {codes, fmt ? (size_t)T * mx_row_bytes(H, fmt) : 0},
+                 {scales, (size_t)T * mx_words(H) * 4}, {sum, n}, {gamma, (size_t)H * 4},
+                 {x, n}, {residual, n}};  // the outputs first
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < (i < 3 ? 7 : 5); ++j)
+      if (r[i].p && r[j].p && overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_add_rmsnorm(x, residual, gamma, eps, T, H, fmt, sum, xn, codes, scales,
                                         static_cast<cudaStream_t>(stream)));
 }
@@ -1167,8 +1180,12 @@ int32_t moe_mx_quantize(const void* x, int32_t groups, int32_t rows, int32_t K, 
   const int32_t st = check_mx(groups, rows, K, fmt);
   if (st != MOE_OK) return st;
   if (groups == 0 || rows == 0) return MOE_OK;
-  if (!x || !codes || !scales || codes == x) return MOE_ERR_INVALID_ARG;
+  if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 32) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)groups * rows;
+  if (overlaps_mx(x, n * K * 2, codes, scales, n, K, fmt) ||
+      overlap(codes, n * mx_row_bytes(K, fmt), scales, n * mx_words(K) * 4))
+    return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_mx_quantize(x, groups, rows, K, fmt, codes, scales,
                                         static_cast<cudaStream_t>(stream)));
 }
@@ -1178,8 +1195,10 @@ int32_t moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t g
   const int32_t st = check_mx(groups, rows, K, fmt);
   if (st != MOE_OK) return st;
   if (groups == 0 || rows == 0) return MOE_OK;
-  if (!x || !codes || !scales || codes == x) return MOE_ERR_INVALID_ARG;
+  if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 32) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)groups * rows;
+  if (overlaps_mx(x, n * K * 2, codes, scales, n, K, fmt)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_mx_dequantize(codes, scales, groups, rows, K, fmt, x,
                                           static_cast<cudaStream_t>(stream)));
 }

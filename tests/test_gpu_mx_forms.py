@@ -262,3 +262,33 @@ def test_two_threads_on_one_stream(T, up, down):
         assert len(got[i]) == 60
         for y in got[i]:
             assert torch.equal(y, wants[i])
+
+
+# ------------------------------------------------------------------ side by side in memory
+@gpu
+def test_outputs_may_lie_beside_what_is_read_but_not_over_it():
+    T, H, K, N, E = 6, 128, 64, 64, 2
+    g = gen(1)
+    buf = torch.empty(3 * T + 1, H, dtype=torch.bfloat16, device=DEV)
+    x, r = buf[:T], buf[T:2 * T]
+    x.copy_(torch.randn(T, H, generator=g).bfloat16())
+    r.copy_(torch.randn(T, H, generator=g).bfloat16())
+    keep = buf[:2 * T].clone()
+    want = ops.add_rmsnorm(x.clone(), r.clone(), fmt="mxfp8")
+    got = ops.add_rmsnorm(x, r, fmt="mxfp8", sum_out=buf[2 * T:3 * T])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert torch.equal(buf[:2 * T], keep)
+    for bad in (buf[1:T + 1], buf[T - 1:2 * T - 1], buf[2 * T - 1:3 * T - 1]):
+        with pytest.raises(RuntimeError, match="INVALID_ARG"):
+            ops.add_rmsnorm(x, r, fmt="mxfp8", sum_out=bad)
+    assert torch.equal(buf[:2 * T], keep)
+    rows = torch.randn(T, K, generator=g).bfloat16().to(DEV)
+    w = torch.randn(E, N, K, generator=g).bfloat16().to(DEV)
+    off = torch.tensor([0, 2, T], dtype=torch.int32, device=DEV)
+    both = torch.empty(2 * T, K, dtype=torch.bfloat16, device=DEV)
+    both[:T].copy_(rows)
+    assert torch.equal(ops.grouped_mm(both[:T], w, off, out=both[T:]), ops.grouped_mm(rows, w, off))
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):
+        ops.grouped_mm(both[:T], w, off, out=both[T - 1:2 * T - 1])
+    assert torch.equal(both[:T], rows)

@@ -1,7 +1,8 @@
-"""Outputs that lie over an operand of the grouped products are refused before any
-CUDA call (the pointers below are not followed)."""
+"""Outputs of the narrow-format operators that lie over what the call reads are refused
+before any CUDA call (the pointers below are not followed)."""
 
 import pytest
+import torch
 
 from routed_moe_layer_b200 import build, ops
 
@@ -63,3 +64,56 @@ def test_expert_rows_mx(L, fmt):
             assert got == expect(over), (at, y)
     assert L.moe_expert_rows_mx(x, xs, T, 7 * P, 8 * P, R, E, H, I, fmt, w13, w13s, w2, w2s, None,
                                 9 * P, x, y_rows, None, 0, None) == INVALID
+
+
+# These have no workspace that could be missing, so only what is refused is tried, and not where
+# a refusal that got lost would make a kernel follow the pointers.
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="pointers that nothing may follow")
+
+
+@no_gpu
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_quantisation(L, fmt):
+    groups, rows, K = 2, 5, 160
+    n = groups * rows
+    row = K if fmt == 1 else K // 2
+    x, c, s = P, 2 * P, 3 * P
+    sizes = {"x": n * K * 2, "c": n * row, "s": n * 2 * 4}
+
+    def both(x, c, s):
+        return [L.moe_mx_quantize(x, groups, rows, K, fmt, c, s, None),
+                L.moe_mx_dequantize(c, s, groups, rows, K, fmt, x, None)]
+    for name, at in (("c", c), ("s", s)):
+        for y, over in touching(at, sizes[name], sizes["x"]):
+            if over:
+                assert both(y, c, s) == [INVALID] * 2
+    for y, over in touching(c, sizes["c"], sizes["s"]):
+        if over:  # the scales over the codes
+            assert L.moe_mx_quantize(x, groups, rows, K, fmt, c, y, None) == INVALID
+
+
+@no_gpu
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_add_rmsnorm(L, fmt):
+    T, H = 5, 192
+    n, row = T * H * 2, H if fmt == 1 else H // 2
+    at = dict(x=P, residual=2 * P, gamma=3 * P, sum=4 * P, xn=5 * P)
+    size = dict(x=n, residual=n, gamma=H * 4, sum=n, xn=n)
+    if fmt:
+        at |= dict(codes=6 * P, scales=7 * P)
+        size |= dict(codes=T * row, scales=2 * T * 4)
+
+    def call(**kw):
+        a = dict(codes=None, scales=None) | at | kw
+        return L.moe_add_rmsnorm(a["x"], a["residual"], a["gamma"], 1e-6, T, H, fmt, a["sum"],
+                                 a["xn"], a["codes"], a["scales"], None)
+    outs = [o for o in ("sum", "xn", "codes", "scales") if o in at]
+    for o in outs:
+        for other in at:
+            if other == o:
+                continue
+            for y, over in touching(at[other], size[other], size[o]):
+                if over and not (o == "sum" and other in ("x", "residual") and y == at[other]):
+                    assert call(**{o: y}) == INVALID, (o, other, y - at[other])
+    # in place over x, whose other rows are the residual's
+    assert call(sum=P, residual=P + H * 2) == INVALID
