@@ -292,3 +292,72 @@ def test_outputs_may_lie_beside_what_is_read_but_not_over_it():
     with pytest.raises(RuntimeError, match="INVALID_ARG"):
         ops.grouped_mm(both[:T], w, off, out=both[T - 1:2 * T - 1])
     assert torch.equal(both[:T], rows)
+
+
+# ------------------------------------------------------------------ bad indices
+INDEXED = [(12, 4, 160, 96, "tokens", "swapped"), (60, 4, 160, 96, "swapped", "swapped"),
+           (900, 4, 160, 96, "pair", "swapped"), (1000, 2, 2176, 160, "pair", "pair")]
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R,E,H,I,up,down", INDEXED)
+def test_experts_with_bad_offsets_report_them_and_stay_inside(R, E, H, I, up, down, fmt):
+    assert (up_form(R, E), rows_form(R, E, H, fmt)) == (up, down)
+    xc, xs, _ = operands(R, H, fmt, 1)
+    w13 = operands(2 * I, H, fmt, 5, lead=E, scale=H ** -0.5)[:2]
+    w2 = operands(H, I, fmt, 6, lead=E, scale=I ** -0.5)[:2]
+    tok = torch.arange(R, dtype=torch.int32, device=DEV).flip(0).contiguous()
+    y, check = guarded((R, H), torch.bfloat16, DEV)
+    n = ops.lib().moe_expert_rows_mx_workspace_bytes(R, H, E, I, ops.MX_FORMATS[fmt], 1)
+    ws, c_ws = guarded((n,), torch.uint8, DEV)
+
+    def call(off):
+        ops.expert_rows_mx(xc, xs, torch.tensor(off, dtype=torch.int32, device=DEV), *w13, *w2, None,
+                           fmt, tok_of=tok, y=y, workspace=ws)
+        return ops.read_device_status(ws)[0]
+    even = [R * e // E for e in range(E + 1)]
+    assert call(even) == 0
+    want = y.clone()
+    for bad in (even[:-1] + [R + 50], [-5] + even[1:], [even[0], R, *even[2:]] if E > 2 else [R, 0, R],
+                [2 ** 30, 2 ** 31 - 1] + [5] * (E - 1), [-2 ** 31] * (E + 1)):
+        assert call(bad) == 6
+        check()
+        c_ws()
+    assert call(even) == 0  # cleared by the next call
+    assert torch.equal(y, want)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R,E,H,I,up,down", INDEXED)
+def test_experts_tokens_and_destinations_outside(R, E, H, I, up, down, fmt):
+    """A token outside counts as zeros, a row whose destination lies outside is not stored; the
+    other rows have the bits of the call without them."""
+    assert (up_form(R, E), rows_form(R, E, H, fmt)) == (up, down)
+    T = R // 2
+    xc, xs, _ = operands(T, H, fmt, 1)
+    w13 = operands(2 * I, H, fmt, 5, lead=E, scale=H ** -0.5)[:2]
+    w2 = operands(H, I, fmt, 6, lead=E, scale=I ** -0.5)[:2]
+    off = torch.tensor([R * e // E for e in range(E + 1)], dtype=torch.int32, device=DEV)
+    tok = torch.randint(0, T, (R,), generator=gen(2)).int()
+    want = ops.expert_rows_mx(xc, xs, off, *w13, *w2, None, fmt, tok_of=tok.to(DEV))
+    none = torch.zeros(R, dtype=torch.bool)
+    for at, t in ((0, -1), (R // 3, T), (R // 2, 2 ** 31 - 1), (R - 1, -2 ** 31)):
+        tok[at], none[at] = t, True
+    dest = torch.randperm(R, generator=gen(3)).int()
+    lost = torch.zeros(R, dtype=torch.bool)
+    free = []
+    for at, to in ((1, -1), (R // 3 + 1, R), (R // 2 + 1, 2 ** 31 - 1), (R - 2, -2 ** 31)):
+        free.append(int(dest[at]))
+        dest[at], lost[at] = to, True
+    y, check = guarded((R, H), torch.bfloat16, DEV)
+    y.fill_(7.0)
+    ops.expert_rows_mx(xc, xs, off, *w13, *w2, dest.to(DEV), fmt, tok_of=tok.to(DEV), y=y)
+    check()
+    kept = ~lost
+    got = y[dest[kept].long().to(DEV)]
+    zero = none[kept].to(DEV)
+    assert (got[zero] == 0).all()
+    assert torch.equal(got[~zero], want[kept.to(DEV)][~zero])
+    assert (y[torch.tensor(free, device=DEV)] == 7).all()
